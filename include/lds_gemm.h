@@ -68,7 +68,16 @@ enum gemm_dtype {
     GEMM_F16_F16 = 2,    /* fp16 A, B;  fp16 C (round to nearest even)     */
     GEMM_F16_F32 = 3,    /* fp16 A, B;  fp32 C                             */
     GEMM_E4M3_F32 = 4,   /* fp8 E4M3 A, B;  fp32 C                         */
-    GEMM_E4M3_BF16 = 5   /* fp8 E4M3 A, B;  bf16 C (round to nearest even) */
+    GEMM_E4M3_BF16 = 5,  /* fp8 E4M3 A, B;  bf16 C (round to nearest even) */
+    GEMM_E4M3_F16 = 6    /* fp8 E4M3 A, B;  fp16 C: gemm_scaled_run only   */
+};
+
+/* Element types of gemm_rmsnorm_run, named input_output. */
+enum gemm_norm_dtype {
+    GEMM_NORM_BF16_BF16 = 0,
+    GEMM_NORM_BF16_E4M3 = 1,
+    GEMM_NORM_F16_F16 = 2,
+    GEMM_NORM_F16_E4M3 = 3
 };
 
 enum gemm_status {
@@ -104,6 +113,73 @@ int gemm_run(gemm_handle_t h, const void *A, const void *B, void *C,
              int64_t M, int64_t N, int64_t K,
              int64_t lda, int64_t ldb, int64_t ldc,
              int layoutA, int layoutB, int dtype, hipStream_t stream);
+
+/* Enqueue C <- diag(SA) * A * B * diag(SB) on `stream`, for E4M3 operands:
+ *     C[m][n] = round( (sum_k a(m,k) * b(k,n)) * SA[m*incA] * SB[n*incB] )
+ * with the sum in fp32, the two factors applied to it in fp32 in that order,
+ * and one rounding to C's type.
+ *   SA, SB       device pointers to fp32 scales, 4-byte aligned: one for each
+ *                row of A and each column of B (incA, incB = 1), or one for
+ *                all of them (0).  They must not overlap C.
+ *   dtype        GEMM_E4M3_F32, GEMM_E4M3_BF16 or GEMM_E4M3_F16.
+ * Everything else is as for gemm_run with E4M3 operands, K == 0 included: the
+ * empty sum is scaled like any other. */
+int gemm_scaled_run(gemm_handle_t h, const void *A, const void *B, void *C,
+                    const float *SA, const float *SB,
+                    int64_t M, int64_t N, int64_t K,
+                    int64_t lda, int64_t ldb, int64_t ldc,
+                    int incA, int incB,
+                    int layoutA, int layoutB, int dtype, hipStream_t stream);
+
+/* Enqueue, on `stream`, the product of 16-bit rows with 4-bit weights that
+ * carry a scale and a zero point for every `group` consecutive k:
+ *     C[m][n] = round( sum_k A[m*lda + k] *
+ *               S[(k/group)*lds + n] * (q(k,n) - Z[(k/group)*ldz + n]) )
+ * summed in fp32, one rounding to C's type.  Meant for few rows (M <= 64: the
+ * weights are read once); any M is computed, the weights being read again for
+ * every 64 rows.
+ *   A            bf16/fp16, K-contiguous, 16-byte aligned; lda a multiple of 8.
+ *   B            q(k,n) = bits 4*(k&1) .. 4*(k&1)+3 of byte (n*ldb + k)/2: two
+ *                weights a byte, K-contiguous, even k in the low half.  16-byte
+ *                aligned; ldb counts weights and is a multiple of 32.
+ *   S            scales of A's type, one row of N for each group of k.
+ *   Z            zero points, unsigned bytes, one row of N for each group; or
+ *                NULL: every zero point is 8.
+ *   K            a multiple of 32; K == 0 writes zeros and reads nothing.
+ *   group        a power of two, 32 or more; the last group may be cut short
+ *                by K, and a group of K or more is one scale for a column.
+ *   lda, ldb >= K; lds, ldz, ldc >= N; each < 2^40.
+ *   dtype        GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_F16_F16 or GEMM_F16_F32.
+ * C is 4-byte (fp32) or 2-byte aligned and overlaps no input. */
+int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const void *S,
+                const void *Z, void *C,
+                int64_t M, int64_t N, int64_t K, int64_t group,
+                int64_t lda, int64_t ldb, int64_t lds, int64_t ldz, int64_t ldc,
+                int dtype, hipStream_t stream);
+
+/* Enqueue the root-mean-square norm of the rows of X, or of X + R, on `stream`:
+ *     h[m][n] = X[m*ldx + n] + R[m*ldr + n]        (without R: X alone)
+ *     y[m][n] = h[m][n] * W[n] / sqrt(mean over n of h[m][n]^2 + eps)
+ *     H[m*ldh + n] = h rounded to X's type
+ *     Y[m*ldy + n] = y rounded to X's type, or, for E4M3 output,
+ *     S[m] = max(max over n of |y[m][n]|, 2^-100) / 448 and
+ *     Y[m*ldy + n] = y[m][n] / S[m] rounded to E4M3,
+ * so that S and Y are the SA and A of gemm_scaled_run.  All arithmetic is
+ * fp32 and y is computed from h before it is rounded.  A row that holds a NaN
+ * or an infinity gives NaNs, in S[m] too.
+ *   X, R, W, H   elements of the input type, 2-byte aligned; R and H may be
+ *                NULL (no residual; h not wanted).
+ *   Y            input type (2-byte aligned) or E4M3; S is used for E4M3 only.
+ *   ldx, ldy >= N, ldr >= N with R, ldh >= N with H; each < 2^40.
+ *   eps >= 0;  M == 0 or N == 0 is a no-op.
+ * H and a 16-bit Y may each stand in the place of X or of R (same address and
+ * leading dimension); no other overlap with an output is allowed.  Rows that
+ * start on 16 bytes (8 for E4M3) take wide accesses. */
+int gemm_rmsnorm_run(gemm_handle_t h, const void *X, const void *R, const void *W,
+                     void *H, void *Y, float *S,
+                     int64_t M, int64_t N,
+                     int64_t ldx, int64_t ldr, int64_t ldh, int64_t ldy,
+                     float eps, int dtype, hipStream_t stream);
 
 /* Release a handle.  NULL is accepted and returns GEMM_OK. */
 int gemm_destroy(gemm_handle_t h);

@@ -4,7 +4,11 @@ Argument marshalling only: every step of C <- A*B runs in the HIP library
 liblds_gemm.so built in this directory.  There is no fallback: if the
 library is missing, every entry point raises.
 
-Names mirror the C ABI: gemm_create, gemm_run, gemm_destroy, gemm_status_str.
+Names mirror the C ABI: gemm_create, gemm_run, gemm_destroy, gemm_status_str,
+and the operators of a quantised linear layer: gemm_rmsnorm_run (norm with the
+residual's addition, 16-bit or scaled E4M3 output), gemm_scaled_run (E4M3
+product with row and column scales) and gemm_w4_run (few rows times 4-bit
+weights).
 Pointers may be passed as integers or as objects with a ``data_ptr()`` method
 (torch tensors); streams as integers, objects with a ``cuda_stream``
 attribute (torch streams) or None for the null stream.
@@ -15,18 +19,21 @@ import os
 __all__ = [
     "GEMM_K_CONTIG", "GEMM_MN_CONTIG",
     "GEMM_BF16_F32", "GEMM_BF16_BF16", "GEMM_F16_F16", "GEMM_F16_F32", "GEMM_E4M3_F32",
-    "GEMM_E4M3_BF16",
+    "GEMM_E4M3_BF16", "GEMM_E4M3_F16",
+    "GEMM_NORM_BF16_BF16", "GEMM_NORM_BF16_E4M3", "GEMM_NORM_F16_F16", "GEMM_NORM_F16_E4M3",
     "GEMM_OK", "GEMM_ERR_INVALID_ARG", "GEMM_ERR_UNSUPPORTED", "GEMM_ERR_DEVICE",
     "GEMM_ERR_LAUNCH", "GemmError", "library_path", "load_library", "gemm_create",
-    "gemm_run", "gemm_destroy", "gemm_status_str", "EXPORTED_SYMBOLS", "Library",
+    "gemm_run", "gemm_scaled_run", "gemm_w4_run", "gemm_rmsnorm_run", "gemm_destroy", "gemm_status_str", "EXPORTED_SYMBOLS", "Library",
     "ablation_library",
 ]
 
 GEMM_K_CONTIG, GEMM_MN_CONTIG = 0, 1
 GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_F16_F16, GEMM_F16_F32 = 0, 1, 2, 3
-GEMM_E4M3_F32, GEMM_E4M3_BF16 = 4, 5
+GEMM_E4M3_F32, GEMM_E4M3_BF16, GEMM_E4M3_F16 = 4, 5, 6
+GEMM_NORM_BF16_BF16, GEMM_NORM_BF16_E4M3, GEMM_NORM_F16_F16, GEMM_NORM_F16_E4M3 = range(4)
 GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED, GEMM_ERR_DEVICE, GEMM_ERR_LAUNCH = range(5)
-EXPORTED_SYMBOLS = ("gemm_create", "gemm_run", "gemm_destroy", "gemm_status_str")
+EXPORTED_SYMBOLS = ("gemm_create", "gemm_run", "gemm_scaled_run", "gemm_w4_run", "gemm_rmsnorm_run",
+                    "gemm_destroy", "gemm_status_str")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "liblds_gemm.so"
@@ -64,7 +71,14 @@ def load_library():
     """Load liblds_gemm.so (raises if it has not been built)."""
     global _lib
     if _lib is None:
-        _lib = _open(library_path())
+        lib = _open(library_path())
+        vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+        lib.gemm_scaled_run.argtypes = [vp] * 6 + [i64] * 6 + [i32] * 5 + [vp]
+        lib.gemm_w4_run.argtypes = [vp] * 6 + [i64] * 9 + [i32, vp]
+        lib.gemm_rmsnorm_run.argtypes = [vp] * 7 + [i64] * 6 + [f32, i32, vp]
+        for f in (lib.gemm_scaled_run, lib.gemm_w4_run, lib.gemm_rmsnorm_run):
+            f.restype = i32
+        _lib = lib
     return _lib
 
 
@@ -116,6 +130,35 @@ def gemm_run(h, A, B, C, M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype, stream
                                    _stream(stream))
 
 
+def _ints(bits, **values):
+    return [_int(v, bits, n) for n, v in values.items()]
+
+
+def gemm_scaled_run(h, A, B, C, SA, SB, M, N, K, lda, ldb, ldc, incA, incB, layoutA, layoutB, dtype,
+                    stream=None) -> int:
+    """Enqueue C <- diag(SA) A B diag(SB) for E4M3 operands; returns the gemm_status code."""
+    return load_library().gemm_scaled_run(
+        h, _ptr(A), _ptr(B), _ptr(C), _ptr(SA), _ptr(SB),
+        *_ints(64, M=M, N=N, K=K, lda=lda, ldb=ldb, ldc=ldc),
+        *_ints(32, incA=incA, incB=incB, layoutA=layoutA, layoutB=layoutB, dtype=dtype), _stream(stream))
+
+
+def gemm_w4_run(h, A, B, S, Z, C, M, N, K, group, lda, ldb, lds, ldz, ldc, dtype, stream=None) -> int:
+    """Enqueue the product of 16-bit rows with 4-bit weights; returns the gemm_status code."""
+    return load_library().gemm_w4_run(
+        h, _ptr(A), _ptr(B), _ptr(S), _ptr(Z), _ptr(C),
+        *_ints(64, M=M, N=N, K=K, group=group, lda=lda, ldb=ldb, lds=lds, ldz=ldz, ldc=ldc),
+        _int(dtype, 32, "dtype"), _stream(stream))
+
+
+def gemm_rmsnorm_run(h, X, R, W, H, Y, S, M, N, ldx, ldr, ldh, ldy, eps, dtype, stream=None) -> int:
+    """Enqueue the RMS norm of X (+ R); returns the gemm_status code."""
+    return load_library().gemm_rmsnorm_run(
+        h, _ptr(X), _ptr(R), _ptr(W), _ptr(H), _ptr(Y), _ptr(S),
+        *_ints(64, M=M, N=N, ldx=ldx, ldr=ldr, ldh=ldh, ldy=ldy), float(eps),
+        _int(dtype, 32, "dtype"), _stream(stream))
+
+
 def gemm_destroy(h) -> int:
     return load_library().gemm_destroy(h)
 
@@ -125,8 +168,9 @@ def gemm_status_str(status: int) -> str:
 
 
 class Library:
-    """The same four entry points bound to one specific build of the library
-    (the default build, or an A/B build from ablation_library())."""
+    """gemm_create, gemm_run, gemm_destroy and gemm_status_str bound to one
+    specific build of the library (the default build, or an A/B build from
+    ablation_library(); an A/B build holds these four and nothing else)."""
 
     def __init__(self, path):
         self.path = path

@@ -12,13 +12,16 @@ Also builds, from the same sources:
 """
 import os
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblds_gemm.so")
 ABLATION_DIR = os.path.join(PKG, "ablation")
-SOURCES = ["gemm_api.hip"]
+SOURCES = ["gemm_api.hip", "gemm_scaled.hip", "gemm_w4.hip", "gemm_norm.hip"]
+VARIANT_SOURCES = ["gemm_api.hip"]     # the A/B builds change gemm_run's kernels
+OBJ_DIR = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC",
          # keep packed fp32 instructions out of the generated code
@@ -72,14 +75,22 @@ def _run(cmd, out, verbose):
 
 def build(verbose: bool = False, extra_flags=(), variant: str = None) -> str:
     """Build the library (or, with `variant`, one ablation build)."""
-    out = LIB
-    flags = list(extra_flags)
     if variant is not None:
         os.makedirs(ABLATION_DIR, exist_ok=True)
         out = variant_path(variant)
-        flags = VARIANTS[variant] + flags
-    cmd = [HIPCC, *FLAGS, *flags, "-shared",
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", out + ".tmp"]
+        cmd = [HIPCC, *FLAGS, *VARIANTS[variant], *extra_flags, "-shared",
+               *[os.path.join(CSRC, s) for s in VARIANT_SOURCES], "-o", out + ".tmp"]
+        return _run(cmd, out, verbose)
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+        objs = list(pool.map(lambda s: build_object(s, verbose, extra_flags), SOURCES))
+    return _run([HIPCC, *FLAGS, "-shared", *objs, "-o", LIB + ".tmp"], LIB, verbose)
+
+
+def build_object(source: str, verbose: bool = False, extra_flags=()) -> str:
+    """One translation unit of the library."""
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    out = os.path.join(OBJ_DIR, os.path.splitext(source)[0] + ".o")
+    cmd = [HIPCC, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, source), "-o", out + ".tmp"]
     return _run(cmd, out, verbose)
 
 
@@ -102,7 +113,6 @@ def build_layout_host(verbose: bool = False):
 
 def build_all(verbose: bool = False):
     """Every build, six hipcc processes at a time."""
-    from concurrent.futures import ThreadPoolExecutor
     jobs = [lambda: build(verbose)] + [lambda n=n: build(verbose, variant=n) for n in VARIANTS] + \
            [lambda: build_layout_host(verbose), lambda: build_hw_probe(verbose)]
     with ThreadPoolExecutor(max_workers=6) as pool:

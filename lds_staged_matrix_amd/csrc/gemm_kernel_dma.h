@@ -146,10 +146,14 @@ __device__ __forceinline__ void read_frags(Frags<T, IN> &f, const char *sA, cons
 
 template <class T, int IN>
 __device__ __forceinline__ void mfma_block(v16f32 (&acc)[T::FM][T::FN], const Frags<T, IN> &f) {
+  if constexpr (IN == IN_E4M3_AS_BF16) {
+    mfma_e4m3_as_bf16<32>(acc, f.a, f.b);
+  } else {
 #pragma unroll
-  for (int i = 0; i < T::FM; i++)
+    for (int i = 0; i < T::FM; i++)
 #pragma unroll
-    for (int j = 0; j < T::FN; j++) acc[i][j] = mfma_step<IN>(f.a[i], f.b[j], acc[i][j]);
+      for (int j = 0; j < T::FN; j++) acc[i][j] = mfma_step<IN>(f.a[i], f.b[j], acc[i][j]);
+  }
 }
 
 // Interleave the LDS reads of the next k-step with the MFMAs of this one:
@@ -194,11 +198,12 @@ __device__ __forceinline__ void wait_tiles(int n) {
 // operand panels overflow the L2 and come from further out: then the loads
 // of tile kt+4 go out as soon as tile kt's stage is free, three tiles ahead
 // of their use instead of one.
-template <class T, int LA, int LB, int IN, int OUT, int NS = 2>
+// SC is empty, or RowColScale for a product whose rows and columns are scaled.
+template <class T, int LA, int LB, int IN, int OUT, int NS = 2, class... SC>
 __global__ __launch_bounds__(T::NT, 1) void lds_gemm_dma_kernel(
     const uint16_t *__restrict__ A, const uint16_t *__restrict__ B, void *__restrict__ C,
     int M, int N, int K, int64_t lda, int64_t ldb, int64_t ldc, int tiles_m, int tiles_n,
-    uint32_t a_bytes, uint32_t b_bytes, int c_vec) {
+    uint32_t a_bytes, uint32_t b_bytes, int c_vec, SC... sc) {
   constexpr int ES = InT<IN>::ES;
   constexpr int KSTEPS = T::BK / InT<IN>::KSTEP;          // MFMA k-steps per K tile
   using OA = OperandTile<T::BM, T::BK, LA, T::NT, ES>;
@@ -335,6 +340,8 @@ __global__ __launch_bounds__(T::NT, 1) void lds_gemm_dma_kernel(
   }
   }
 
+  if constexpr (sizeof...(SC) > 0)
+    scale_acc<32>(acc, m0 + wm * T::TM, n0 + wn * T::TN, M, N, lane, sc...);
   if constexpr (LSM_DMA_ROW_EPI) {
     if (c_vec) {
       __syncthreads();                     // every wave is past its last LDS read

@@ -112,11 +112,12 @@ __device__ __forceinline__ void wg_barrier() {
 __device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // Ping-pong tile: 256 x 256 x 64, waves 2 (M) x 4 (N), wave tile 128 x 64.
-template <class T, int LA, int LB, int IN, int OUT, int MF = 32>
+// SC is empty, or RowColScale for a product whose rows and columns are scaled.
+template <class T, int LA, int LB, int IN, int OUT, int MF = 32, class... SC>
 __global__ __launch_bounds__(T::NT, 1) void lds_gemm_pingpong_kernel(
     const uint16_t *__restrict__ A, const uint16_t *__restrict__ B, void *__restrict__ C,
     int M, int N, int K, int64_t lda, int64_t ldb, int64_t ldc, int tiles_m, int tiles_n,
-    uint32_t a_bytes, uint32_t b_bytes, int c_vec) {
+    uint32_t a_bytes, uint32_t b_bytes, int c_vec, SC... sc) {
   static_assert(T::WM == 2 && T::NT == 512, "two groups of four waves");
   static_assert(MF == 32 || MF == 16, "32 x 32 or 16 x 16 MFMAs");
 #if LSM_PP_TIMELINE
@@ -392,16 +393,21 @@ __global__ __launch_bounds__(T::NT, 1) void lds_gemm_pingpong_kernel(
       // ---- compute phase C(kt)
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int kk = 0; kk < KSTEPS; ++kk)
+      for (int kk = 0; kk < KSTEPS; ++kk) {
+        if constexpr (IN == IN_E4M3_AS_BF16) {
+          mfma_e4m3_as_bf16<MF>(acc, fa[kk], fb[kk]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < FM; i++)
+          for (int i = 0; i < FM; i++)
 #pragma unroll
-          for (int j = 0; j < FN; j++) {
-            if constexpr (MF == 32)
-              acc[i][j] = mfma_step<IN>(fa[kk][i], fb[kk][j], acc[i][j]);
-            else
-              acc[i][j] = mfma16_step<IN>(fa[kk][i], fb[kk][j], acc[i][j]);
-          }
+            for (int j = 0; j < FN; j++) {
+              if constexpr (MF == 32)
+                acc[i][j] = mfma_step<IN>(fa[kk][i], fb[kk][j], acc[i][j]);
+              else
+                acc[i][j] = mfma16_step<IN>(fa[kk][i], fb[kk][j], acc[i][j]);
+            }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < FM; i++)
 #pragma unroll
@@ -429,6 +435,9 @@ __global__ __launch_bounds__(T::NT, 1) void lds_gemm_pingpong_kernel(
 #if LSM_PP_TIMELINE
   const unsigned long long t_loop = PP_CLOCK();
 #endif
+
+  if constexpr (sizeof...(SC) > 0)
+    scale_acc<MF>(acc, m0 + wm * T::TM, n0 + wn * T::TN, M, N, lane, sc...);
 
   // The LDS is free once every wave is past its last fragment read.
   if (c_vec) {

@@ -45,11 +45,12 @@ struct SkinnyTile {
   static_assert(BM % 32 == 0 && BN % 32 == 0, "split-K tile geometry");
 };
 
-template <class T, int LA, int LB, int IN, int OUT>
+// SC is empty, or RowColScale for a product whose rows and columns are scaled.
+template <class T, int LA, int LB, int IN, int OUT, class... SC>
 __global__ __launch_bounds__(T::NT, 1) void lds_gemm_skinny_kernel(
     const uint16_t *__restrict__ A, const uint16_t *__restrict__ B, void *__restrict__ C,
     int M, int N, int K, int64_t lda, int64_t ldb, int64_t ldc, int tiles_m, int tiles_n,
-    uint32_t a_bytes, uint32_t b_bytes) {
+    uint32_t a_bytes, uint32_t b_bytes, SC... sc) {
   constexpr int ES = InT<IN>::ES;
   constexpr int KSTEPS = T::BK / InT<IN>::KSTEP / T::WAVES;   // MFMA k-steps per wave per stage
   static_assert(KSTEPS >= 1 && KSTEPS * InT<IN>::KSTEP * T::WAVES == T::BK, "stage splits over the waves");
@@ -178,6 +179,7 @@ __global__ __launch_bounds__(T::NT, 1) void lds_gemm_skinny_kernel(
 #pragma unroll
         for (int w = 1; w < T::WAVES; w++) v += red[red_at(w, i, j, r)];
         const int row = row0 + q;
+        if constexpr (sizeof...(SC) > 0) v = scale_entry(v, row, col, M, N, sc...);
         if (row < M && col < N) store_out<OUT>(C, (int64_t)row * ldc + col, v);
       }
     }

@@ -1,0 +1,103 @@
+// gemm_scaled.hip -- gemm_scaled_run: the E4M3 product whose rows and columns
+// carry fp32 scales.  The kernels are gemm_run's, with the scales applied to
+// the fp32 sums before they are rounded (scale_acc in gemm_common.h), and the
+// few-rows kernel of gemm_kernel_rows.h.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gemm_kernel_rows.h"
+#include "gemm_launch.h"
+
+namespace lsm {
+
+// An fp32 output multiplies its operands as bf16, whose MFMAs sum in fp32
+// throughout (see e4m3_part_as_bf16); 16-bit outputs, rounded to 2^-8 or 2^-11,
+// take the fp8 MFMAs at twice the rate -- except where HBM is the bound anyway
+// (few rows, IN16).
+template <class T, int KIND, int IN16 = IN_E4M3>
+static hipError_t launch_scaled(const Args &a, int la, int lb, int dtype, hipStream_t s, const RowColScale &sc) {
+  switch (dtype) {
+    case GEMM_E4M3_F32: return launch_layout<T, KIND, IN_E4M3_AS_BF16, OUT_F32, RowColScale>(a, la, lb, s, sc);
+    case GEMM_E4M3_BF16: return launch_layout<T, KIND, IN16, OUT_BF16, RowColScale>(a, la, lb, s, sc);
+    default: return launch_layout<T, KIND, IN16, OUT_F16, RowColScale>(a, la, lb, s, sc);
+  }
+}
+
+template <int RB, int NT, int OUT>
+static hipError_t launch_rows(const Args &a, int waves, hipStream_t stream, RowColScale sc) {
+  const char *A = (const char *)a.A, *B = (const char *)a.B;
+  void *C = a.C;
+  int M = a.M, N = a.N, K = a.K;
+  int64_t lda = a.lda, ldb = a.ldb, ldc = a.ldc;
+  int tiles_m = (int)ceil_div(a.M, 16 * RB);
+  const int64_t tiles = tiles_m * ceil_div(a.N, 16 * NT);
+  void *params[] = {&A, &B, &C, &M, &N, &K, &lda, &ldb, &ldc, &tiles_m, &sc};
+  return hipLaunchKernel((const void *)lds_gemm_rows_e4m3_kernel<RB, NT, OUT>, dim3((unsigned)tiles),
+                         dim3(64u * waves), params, (size_t)waves * RB * NT * 1024, stream);
+}
+
+template <int RB, int NT>
+static hipError_t launch_rows_out(const Args &a, int waves, int dtype, hipStream_t s, const RowColScale &sc) {
+  switch (dtype) {
+    case GEMM_E4M3_F32: return launch_rows<RB, NT, OUT_F32>(a, waves, s, sc);
+    case GEMM_E4M3_BF16: return launch_rows<RB, NT, OUT_BF16>(a, waves, s, sc);
+    default: return launch_rows<RB, NT, OUT_F16>(a, waves, s, sc);
+  }
+}
+
+// Column blocks by N: the widest tile that still makes a workgroup for every
+// CU; then as many waves as K has blocks for, up to 16 and to 64 KiB of
+// partial sums.
+template <int RB>
+static hipError_t dispatch_rows(const Args &a, int dtype, hipStream_t s, const RowColScale &sc) {
+  const int64_t rows = ceil_div(a.M, 16 * RB);
+  const int nt = rows * ceil_div(a.N, 64) >= 256 ? 4 : rows * ceil_div(a.N, 32) >= 256 ? 2 : 1;
+  int waves = 1;
+  while (waves < 16 && 2 * waves * RB * nt <= 64 && 2 * waves * kRowsBlockK <= a.K) waves *= 2;
+  if (nt == 4) return launch_rows_out<RB, 4>(a, waves, dtype, s, sc);
+  if (nt == 2) return launch_rows_out<RB, 2>(a, waves, dtype, s, sc);
+  return launch_rows_out<RB, 1>(a, waves, dtype, s, sc);
+}
+
+// The shape classes of gemm_run's E4M3 products; at most 32 rows with both
+// operands K-contiguous take the few-rows kernel.
+static hipError_t dispatch_scaled(const Args &a, int la, int lb, int dtype, hipStream_t s, const RowColScale &sc) {
+  if (a.M <= 16 && la == KC && lb == KC) return dispatch_rows<1>(a, dtype, s, sc);
+  if (a.M <= 32 && la == KC && lb == KC) return dispatch_rows<2>(a, dtype, s, sc);
+  if (a.M <= 32) return launch_scaled<SkinnyStream8, SKINNY, IN_E4M3_AS_BF16>(a, la, lb, dtype, s, sc);
+  if (ceil_div(a.M, 256) * ceil_div(a.N, 256) >= 256)
+    return launch_scaled<PingPong8, PINGPONG>(a, la, lb, dtype, s, sc);
+  if (ceil_div(a.M, 128) * ceil_div(a.N, 128) >= 256)
+    return launch_scaled<DmaMid8, DMA>(a, la, lb, dtype, s, sc);
+  if (small_tile_four_stages(a, 1)) return launch_scaled<DmaSmall8, DMA4>(a, la, lb, dtype, s, sc);
+  return launch_scaled<DmaSmall8, DMA>(a, la, lb, dtype, s, sc);
+}
+
+}  // namespace lsm
+
+extern "C" int gemm_scaled_run(gemm_handle_t h, const void *A, const void *B, void *C, const float *SA,
+                               const float *SB, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                               int64_t ldc, int incA, int incB, int layoutA, int layoutB, int dtype,
+                               hipStream_t stream) {
+  using namespace lsm;
+  if (!h || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+  if (dtype != GEMM_E4M3_F32 && dtype != GEMM_E4M3_BF16 && dtype != GEMM_E4M3_F16) return GEMM_ERR_INVALID_ARG;
+  if ((incA != 0 && incA != 1) || (incB != 0 && incB != 1)) return GEMM_ERR_INVALID_ARG;
+  const int64_t out_size = dtype == GEMM_E4M3_F32 ? 4 : 2;
+  Args args;
+  const int st = check_product(A, B, C, M, N, K, lda, ldb, ldc, layoutA, layoutB, 1, out_size, args);
+  if (st != GEMM_OK || M == 0 || N == 0) return st;
+  if (!SA || !SB) return GEMM_ERR_INVALID_ARG;
+  if (((uintptr_t)SA & 3) || ((uintptr_t)SB & 3)) return GEMM_ERR_UNSUPPORTED;
+  const int64_t c_bytes = footprint_bytes(M, ldc, N, out_size);
+  if (ranges_overlap(C, c_bytes, SA, incA ? 4 * M : 4) || ranges_overlap(C, c_bytes, SB, incB ? 4 * N : 4))
+    return GEMM_ERR_INVALID_ARG;
+  if (!dma_ok(args, layoutA, layoutB, 1)) return GEMM_ERR_UNSUPPORTED;
+
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess || dev != h->device) return GEMM_ERR_DEVICE;
+  if (dispatch_scaled(args, layoutA, layoutB, dtype, stream, RowColScale{SA, SB, incA, incB}) != hipSuccess)
+    return GEMM_ERR_LAUNCH;
+  return GEMM_OK;
+}

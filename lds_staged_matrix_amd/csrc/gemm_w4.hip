@@ -1,0 +1,93 @@
+// gemm_w4.hip -- gemm_w4_run: the product of a few 16-bit rows with 4-bit
+// weights (kernel in gemm_kernel_rows.h).
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gemm_kernel_rows.h"
+#include "gemm_launch.h"
+
+namespace lsm {
+
+template <int IN, int RB, int NT, int GS>
+static hipError_t launch_w4(const W4Args &p, int waves, hipStream_t stream) {
+  W4Args a = p;
+  a.tiles_m = (int)ceil_div(p.M, 16 * RB);
+  const int64_t tiles = a.tiles_m * ceil_div(p.N, 16 * NT);
+  void *params[] = {&a};
+  return hipLaunchKernel((const void *)lds_gemm_w4_kernel<IN, RB, NT, GS>, dim3((unsigned)tiles),
+                         dim3(64u * waves), params, (size_t)waves * RB * NT * 1024, stream);
+}
+
+template <int IN, int RB, int NT>
+static hipError_t launch_w4_group(const W4Args &p, int waves, hipStream_t s) {
+  if (p.gshift == 5) return launch_w4<IN, RB, NT, 1>(p, waves, s);
+  if (p.gshift == 6) return launch_w4<IN, RB, NT, 2>(p, waves, s);
+  return launch_w4<IN, RB, NT, 4>(p, waves, s);
+}
+
+// Row blocks by M, column blocks by N: the widest tile that still makes a
+// workgroup for every CU; then as many waves as K has blocks for, up to 16 and
+// to 64 KiB of partial sums.
+template <int IN, int RB>
+static hipError_t launch_w4_rows(const W4Args &p, hipStream_t s) {
+  const int64_t rows = ceil_div(p.M, 16 * RB);
+  const int nt = rows * ceil_div(p.N, 64) >= 256 ? 4 : rows * ceil_div(p.N, 32) >= 256 ? 2 : 1;
+  int waves = 1;
+  while (waves < 16 && 2 * waves * RB * nt <= 64 && 2 * waves * kRowsBlockK <= p.K) waves *= 2;
+  if (nt == 4) return launch_w4_group<IN, RB, 4>(p, waves, s);
+  if (nt == 2) return launch_w4_group<IN, RB, 2>(p, waves, s);
+  return launch_w4_group<IN, RB, 1>(p, waves, s);
+}
+
+template <int IN>
+static hipError_t dispatch_w4(const W4Args &p, hipStream_t s) {
+  if (p.M <= 16) return launch_w4_rows<IN, 1>(p, s);
+  if (p.M <= 32) return launch_w4_rows<IN, 2>(p, s);
+  return launch_w4_rows<IN, 4>(p, s);
+}
+
+}  // namespace lsm
+
+extern "C" int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const void *S, const void *Z, void *C,
+                           int64_t M, int64_t N, int64_t K, int64_t group, int64_t lda, int64_t ldb, int64_t lds,
+                           int64_t ldz, int64_t ldc, int dtype, hipStream_t stream) {
+  using namespace lsm;
+  if (!h || M < 0 || N < 0 || K < 0 || group < 1) return GEMM_ERR_INVALID_ARG;
+  if (dtype < GEMM_BF16_F32 || dtype > GEMM_F16_F32) return GEMM_ERR_INVALID_ARG;
+  const bool out_f32 = dtype == GEMM_BF16_F32 || dtype == GEMM_F16_F32;
+  if (M == 0 || N == 0) return GEMM_OK;
+  if (!C || (K > 0 && (!A || !B || !S))) return GEMM_ERR_INVALID_ARG;
+  if (ldc < N || (K > 0 && (lda < K || ldb < K || lds < N || (Z && ldz < N)))) return GEMM_ERR_INVALID_ARG;
+
+  const int64_t kMaxDim = (int64_t)1 << 30, kMaxLd = (int64_t)1 << 40;
+  if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return GEMM_ERR_UNSUPPORTED;
+  if (lda >= kMaxLd || ldb >= kMaxLd || lds >= kMaxLd || ldz >= kMaxLd || ldc >= kMaxLd)
+    return GEMM_ERR_UNSUPPORTED;
+  // groups of a power of two of at least 32, and whole 32s of K
+  if (group < 32 || (group & (group - 1)) || group > kMaxDim || K % 32) return GEMM_ERR_UNSUPPORTED;
+  if (ceil_div(M, 16) * ceil_div(N, 16) >= ((int64_t)1 << 31)) return GEMM_ERR_UNSUPPORTED;
+  if ((uintptr_t)C & (out_f32 ? 3 : 1)) return GEMM_ERR_UNSUPPORTED;
+  if (K > 0 && (((uintptr_t)A & 15) || ((uintptr_t)B & 15) || ((uintptr_t)S & 1) || lda % 8 || ldb % 32))
+    return GEMM_ERR_UNSUPPORTED;
+
+  const int64_t G = ceil_div(K, group);
+  const int64_t c_bytes = footprint_bytes(M, ldc, N, out_f32 ? 4 : 2);
+  const int64_t a_bytes = K > 0 ? footprint_bytes(M, lda, K, 2) : 0;
+  const int64_t b_bytes = K > 0 ? footprint_bytes(N, ldb / 2, K / 2, 1) : 0;
+  const int64_t s_bytes = K > 0 ? footprint_bytes(G, lds, N, 2) : 0;
+  const int64_t z_bytes = K > 0 && Z ? footprint_bytes(G, ldz, N, 1) : 0;
+  if (c_bytes < 0 || a_bytes < 0 || b_bytes < 0 || s_bytes < 0 || z_bytes < 0) return GEMM_ERR_UNSUPPORTED;
+  if (K > 0 && (ranges_overlap(C, c_bytes, A, a_bytes) || ranges_overlap(C, c_bytes, B, b_bytes) ||
+                ranges_overlap(C, c_bytes, S, s_bytes) || (Z && ranges_overlap(C, c_bytes, Z, z_bytes))))
+    return GEMM_ERR_INVALID_ARG;
+
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess || dev != h->device) return GEMM_ERR_DEVICE;
+  const W4Args p{(const uint16_t *)A, (const uint8_t *)B, (const uint16_t *)S, (const uint8_t *)Z, C,
+                 (int)M, (int)N, (int)K, (int)G, __builtin_ctzll((unsigned long long)group),
+                 lda, ldb / 2, lds, ldz, ldc, 1, out_f32 ? 1 : 0};
+  const bool bf16 = dtype == GEMM_BF16_F32 || dtype == GEMM_BF16_BF16;
+  const hipError_t e = bf16 ? dispatch_w4<IN_BF16>(p, stream) : dispatch_w4<IN_F16>(p, stream);
+  return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
