@@ -148,7 +148,7 @@ int gemm_scaled_run(gemm_handle_t h, const void *A, const void *B, void *C,
  *   K            a multiple of 32; K == 0 writes zeros and reads nothing.
  *   group        a power of two, 32 or more; the last group may be cut short
  *                by K, and a group of K or more is one scale for a column.
- *   lda, ldb >= K; lds, ldz, ldc >= N; each < 2^40.
+ *   lda, ldb >= K, lda < 2^24, ldb < 2^25; lds, ldz, ldc >= N and < 2^40.
  *   dtype        GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_F16_F16 or GEMM_F16_F32.
  * C is 4-byte (fp32) or 2-byte aligned and overlaps no input. */
 int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const void *S,

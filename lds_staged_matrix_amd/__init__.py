@@ -15,6 +15,7 @@ attribute (torch streams) or None for the null stream.
 """
 import ctypes
 import os
+import struct
 
 __all__ = [
     "GEMM_K_CONTIG", "GEMM_MN_CONTIG",
@@ -85,9 +86,10 @@ def load_library():
 def _ptr(x):
     if x is None:
         return None
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
-    return int(x)
+    except AttributeError:
+        return int(x)
 
 
 def _int(x, bits, name):
@@ -99,19 +101,36 @@ def _int(x, bits, name):
     return v
 
 
-def _sizes(M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype):
-    return ([_int(v, 64, n) for v, n in zip((M, N, K, lda, ldb, ldc),
-                                             ("M", "N", "K", "lda", "ldb", "ldc"))] +
-            [_int(v, 32, n) for v, n in zip((layoutA, layoutB, dtype),
-                                             ("layoutA", "layoutB", "dtype"))])
+class _Ints:
+    """The integer parameters of an entry point, in order: `wide` int64_t, then
+    `narrow` int32_t ones.  A small call's time is mostly its host part, so all
+    are converted and checked in one go; one that does not fit raises."""
+
+    def __init__(self, wide, narrow):
+        self.names = [(n, 64) for n in wide.split()] + [(n, 32) for n in narrow.split()]
+        fmt = struct.Struct("=%dq%di" % (len(wide.split()), len(narrow.split())))
+        self.pack, self.unpack = fmt.pack, fmt.unpack
+
+    def __call__(self, *values):
+        try:
+            return self.unpack(self.pack(*values))
+        except struct.error:        # too large, or not an integer type
+            return [_int(v, bits, name) for v, (name, bits) in zip(values, self.names)]
+
+
+_RUN = _Ints("M N K lda ldb ldc", "layoutA layoutB dtype")
+_SCALED = _Ints("M N K lda ldb ldc", "incA incB layoutA layoutB dtype")
+_W4 = _Ints("M N K group lda ldb lds ldz ldc", "dtype")
+_NORM = _Ints("M N ldx ldr ldh ldy", "dtype")
 
 
 def _stream(s):
     if s is None:
         return None
-    if hasattr(s, "cuda_stream"):
+    try:
         return s.cuda_stream
-    return int(s)
+    except AttributeError:
+        return int(s)
 
 
 def gemm_create():
@@ -126,12 +145,8 @@ def gemm_create():
 def gemm_run(h, A, B, C, M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype, stream=None) -> int:
     """Enqueue C <- A*B; returns the gemm_status code (0 on success)."""
     return load_library().gemm_run(h, _ptr(A), _ptr(B), _ptr(C),
-                                   *_sizes(M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype),
+                                   *_RUN(M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype),
                                    _stream(stream))
-
-
-def _ints(bits, **values):
-    return [_int(v, bits, n) for n, v in values.items()]
 
 
 def gemm_scaled_run(h, A, B, C, SA, SB, M, N, K, lda, ldb, ldc, incA, incB, layoutA, layoutB, dtype,
@@ -139,24 +154,20 @@ def gemm_scaled_run(h, A, B, C, SA, SB, M, N, K, lda, ldb, ldc, incA, incB, layo
     """Enqueue C <- diag(SA) A B diag(SB) for E4M3 operands; returns the gemm_status code."""
     return load_library().gemm_scaled_run(
         h, _ptr(A), _ptr(B), _ptr(C), _ptr(SA), _ptr(SB),
-        *_ints(64, M=M, N=N, K=K, lda=lda, ldb=ldb, ldc=ldc),
-        *_ints(32, incA=incA, incB=incB, layoutA=layoutA, layoutB=layoutB, dtype=dtype), _stream(stream))
+        *_SCALED(M, N, K, lda, ldb, ldc, incA, incB, layoutA, layoutB, dtype), _stream(stream))
 
 
 def gemm_w4_run(h, A, B, S, Z, C, M, N, K, group, lda, ldb, lds, ldz, ldc, dtype, stream=None) -> int:
     """Enqueue the product of 16-bit rows with 4-bit weights; returns the gemm_status code."""
-    return load_library().gemm_w4_run(
-        h, _ptr(A), _ptr(B), _ptr(S), _ptr(Z), _ptr(C),
-        *_ints(64, M=M, N=N, K=K, group=group, lda=lda, ldb=ldb, lds=lds, ldz=ldz, ldc=ldc),
-        _int(dtype, 32, "dtype"), _stream(stream))
+    return load_library().gemm_w4_run(h, _ptr(A), _ptr(B), _ptr(S), _ptr(Z), _ptr(C),
+                                      *_W4(M, N, K, group, lda, ldb, lds, ldz, ldc, dtype), _stream(stream))
 
 
 def gemm_rmsnorm_run(h, X, R, W, H, Y, S, M, N, ldx, ldr, ldh, ldy, eps, dtype, stream=None) -> int:
     """Enqueue the RMS norm of X (+ R); returns the gemm_status code."""
-    return load_library().gemm_rmsnorm_run(
-        h, _ptr(X), _ptr(R), _ptr(W), _ptr(H), _ptr(Y), _ptr(S),
-        *_ints(64, M=M, N=N, ldx=ldx, ldr=ldr, ldh=ldh, ldy=ldy), float(eps),
-        _int(dtype, 32, "dtype"), _stream(stream))
+    M, N, ldx, ldr, ldh, ldy, dtype = _NORM(M, N, ldx, ldr, ldh, ldy, dtype)
+    return load_library().gemm_rmsnorm_run(h, _ptr(X), _ptr(R), _ptr(W), _ptr(H), _ptr(Y), _ptr(S), M, N, ldx, ldr,
+                                           ldh, ldy, eps, dtype, _stream(stream))
 
 
 def gemm_destroy(h) -> int:
@@ -186,7 +197,7 @@ class Library:
     def gemm_run(self, h, A, B, C, M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype,
                  stream=None) -> int:
         return self._lib.gemm_run(h, _ptr(A), _ptr(B), _ptr(C),
-                                  *_sizes(M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype),
+                                  *_RUN(M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype),
                                   _stream(stream))
 
     def gemm_destroy(self, h) -> int:

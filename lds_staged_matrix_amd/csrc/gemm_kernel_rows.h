@@ -4,29 +4,54 @@
 // With M <= 64 rows the product reads every weight once and does little with
 // it, so the time is the weights' bytes over the HBM rate, as long as enough
 // loads are in flight on every CU and nothing else takes longer.
-//  * No LDS staging: a weight is used by one wave only, so it goes straight
-//    from memory into that wave's MFMA operand registers, 16 bytes a lane and
-//    load.  The order of k inside a product is free as long as both operands
-//    agree, so the loads need no transposition.
 //  * A workgroup owns 16 * NT columns and 16 * RB rows of C; its waves split K
 //    among them in blocks of 128, interleaved, so that the waves of a workgroup
 //    together read whole lines of each weight row.  Splitting K inside the
 //    workgroup is what puts 16 waves on every CU when N is a few thousand; the
 //    partial sums meet in LDS and are added in wave order, so a result does not
 //    depend on timing.
-//  * Each wave loads its next block before it multiplies the present one.
-// The activations come from the L2 in fragment form: 16 * RB rows of 128 k
-// for 16 * NT columns of weights.
+//  * Loads take a block row by row: the lanes of a quarter wave read 256 (64,
+//    128) consecutive bytes.  In the order of the MFMA operands, 16 lanes would
+//    each read 16 bytes of another row, and the address path, one line at a
+//    time, would feed a CU no more than 16 bytes a clock, which the
+//    activations alone exceed (measured: 64 rows x 8192 x 8192 took 39.7 us).
+//    The registers go through a slice of LDS of the wave's own, in the
+//    swizzled layout of lds_layout.h, and come back as operands; a wave's LDS
+//    instructions run in order, so no barrier is needed.
+//  * A wave's next block is loaded while it multiplies the present one.
+// The activations come from the L2: RB * 16 rows for 16 * NT columns.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "gemm_common.h"
 
 namespace lsm {
 
 constexpr int kRowsBlockK = 128;         // k of one load block
+
+// The most waves of a workgroup: 128 registers a lane for 16 waves, 256 for
+// eight, and 160 KiB of LDS for the waves' slices (which the partial sums reuse).
+constexpr int rows_max_waves(int rb, int nt, int slice) {
+  int w = rb >= 3 || rb * nt >= 8 ? 8 : 16;
+  while (w * slice > 160 * 1024) w /= 2;
+  return w;
+}
+
+// Orders a wave's own LDS writes and reads, lane against lane, in the compiler
+// (the hardware runs them in order).
+__device__ __forceinline__ void wave_lds_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// LDS bytes of one wave's slice: `arows` rows of A and `bcols` columns of B, one block of each.
+constexpr int rows_slice_bytes(int arows, int a_es, int bcols, int b_bits) {
+  return arows * kRowsBlockK * a_es + bcols * kRowsBlockK * b_bits / 8;
+}
 
 // The workgroup's partial sums, added in wave order through `red` (waves * RB
 // * NT KiB of LDS); `store(m, n, v)` takes each entry of the 16 RB x 16 NT
@@ -59,24 +84,50 @@ __device__ __forceinline__ void store_rows(void *C, int64_t idx, float v) {
 // ------------------------------------------------------------------- E4M3
 //
 // C[m][n] = sum_k a(m,k) b(k,n) * sc.a[m] * sc.b[n], both operands
-// K-contiguous, K a multiple of 16.  Lane (c = lane & 15, g = lane >> 4) holds
-// the 32 bytes at k = 32 g of its block for row c of A and column c of B.
-template <int RB, int NT, int OUT>
-__global__ __launch_bounds__(64 / (RB * NT) >= 16 ? 1024 : 64 * (64 / (RB * NT))) void lds_gemm_rows_e4m3_kernel(
+// K-contiguous, K a multiple of 16.  AR (8, 16 or 32): rows of A that are
+// loaded; RB = 1 of 16 rows or 2.
+template <int AR, int NT>
+struct RowsE4M3 {
+  static constexpr int RB = AR <= 16 ? 1 : AR / 16;
+  static constexpr int SLICE = rows_slice_bytes(AR, 1, 16 * NT, 8);
+  static constexpr int MAX_WAVES = rows_max_waves(RB, NT, SLICE);
+};
+
+template <int AR, int NT, int OUT>
+__global__ __launch_bounds__((64 * RowsE4M3<AR, NT>::MAX_WAVES)) void lds_gemm_rows_e4m3_kernel(
     const char *__restrict__ A, const char *__restrict__ B, void *__restrict__ C, int M, int N, int K,
-    int64_t lda, int64_t ldb, int64_t ldc, int tiles_m, RowColScale sc) {
-  extern __shared__ float red[];
+    uint32_t lda, uint32_t ldb, int64_t ldc, int tiles_m, RowColScale sc) {
+  using T = RowsE4M3<AR, NT>;
+  constexpr int RB = T::RB, LA = AR / 8, LB = 2 * NT;   // loads of 8 rows x 128 bytes
+  constexpr int ROW = kRowsBlockK;                      // bytes of a row's block
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int id = xcd_logical_id(blockIdx.x, gridDim.x);
   const int m0 = (id % tiles_m) * 16 * RB, n0 = (id / tiles_m) * 16 * NT;
 
   // Rows and columns past the end read the last one; their sums are not stored.
-  const char *arow[RB], *brow[NT];
+  const char *abase = A + (int64_t)m0 * lda, *bbase = B + (int64_t)n0 * ldb;
+  const uint32_t amax = (uint32_t)(M - 1 - m0) * lda, bmax = (uint32_t)(N - 1 - n0) * ldb;
+  const int lrow = lane >> 3, lchunk = lane & 7;        // of a load
+  char *slice = smem + wave * T::SLICE, *sa = slice + LB * 1024;
+
+  u32x4 a[LA], b[LB];
+  auto load = [&](int kb) {
+    const int k = kb * kRowsBlockK + 16 * lchunk;
+    // a chunk at k >= K reads the row's start and counts as zero below
+    const uint32_t o = k < K ? (uint32_t)k : 0;
 #pragma unroll
-  for (int i = 0; i < RB; i++) arow[i] = A + (int64_t)min(m0 + 16 * i + c, M - 1) * lda;
+    for (int i = 0; i < LB; i++) b[i] = *(const u32x4 *)(bbase + (min((uint32_t)(8 * i + lrow) * ldb, bmax) + o));
 #pragma unroll
-  for (int t = 0; t < NT; t++) brow[t] = B + (int64_t)min(n0 + 16 * t + c, N - 1) * ldb;
+    for (int i = 0; i < LA; i++) a[i] = *(const u32x4 *)(abase + (min((uint32_t)(8 * i + lrow) * lda, amax) + o));
+  };
+  // operand of row r (of a slice part): the 32 bytes at k = 32 g
+  auto frag = [&](const char *part, int r) {
+    const u32x4 lo = *(const u32x4 *)(part + kc_chunk_offset(r, 2 * g, ROW));
+    const u32x4 hi = *(const u32x4 *)(part + kc_chunk_offset(r, 2 * g + 1, ROW));
+    return __builtin_bit_cast(v8i32, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
 
   v4f32 acc[RB][NT];
 #pragma unroll
@@ -84,56 +135,40 @@ __global__ __launch_bounds__(64 / (RB * NT) >= 16 ? 1024 : 64 * (64 / (RB * NT))
 #pragma unroll
     for (int t = 0; t < NT; t++) acc[i][t] = v4f32{0.f, 0.f, 0.f, 0.f};
 
-  struct Block {
-    u32x4 a[RB][2], b[NT][2];
-  };
-  auto load = [&](Block &f, int kb) {
-    const int k = kb * kRowsBlockK + 32 * g;
-    // a chunk at k >= K reads the row's start and counts as zero below
-    const int o0 = k < K ? k : 0, o1 = k + 16 < K ? k + 16 : 0;
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-      f.b[t][0] = *(const u32x4 *)(brow[t] + o0);
-      f.b[t][1] = *(const u32x4 *)(brow[t] + o1);
-    }
-#pragma unroll
-    for (int i = 0; i < RB; i++) {
-      f.a[i][0] = *(const u32x4 *)(arow[i] + o0);
-      f.a[i][1] = *(const u32x4 *)(arow[i] + o1);
-    }
-  };
-  auto frag = [&](const u32x4 (&p)[2]) {
-    return __builtin_bit_cast(v8i32, __builtin_shufflevector(p[0], p[1], 0, 1, 2, 3, 4, 5, 6, 7));
-  };
-
   const int blocks = (K + kRowsBlockK - 1) / kRowsBlockK;
-  Block cur;
-  if (wave < blocks) load(cur, wave);
-  for (int kb = wave; kb < blocks; kb += waves) {
-    Block nxt;
-    if (kb + waves < blocks) load(nxt, kb + waves);
-    if ((kb + 1) * kRowsBlockK > K) {      // zeros on both sides: a NaN may stand at the row's start
-      const int k = kb * kRowsBlockK + 32 * g;
-      const u32x4 zero = {0, 0, 0, 0};
+  auto block = [&](int kb, auto last) {
+    constexpr bool LAST = decltype(last)::value;
+    if constexpr (LAST) {
+      if (kb * kRowsBlockK + 16 * lchunk >= K) {        // zeros on both sides: a NaN may stand at the row's start
 #pragma unroll
-      for (int h = 0; h < 2; h++)
-        if (k + 16 * h >= K) {
+        for (int i = 0; i < LB; i++) b[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int t = 0; t < NT; t++) cur.b[t][h] = zero;
-#pragma unroll
-          for (int i = 0; i < RB; i++) cur.a[i][h] = zero;
-        }
+        for (int i = 0; i < LA; i++) a[i] = u32x4{0, 0, 0, 0};
+      }
     }
+    wave_lds_order();
+#pragma unroll
+    for (int i = 0; i < LB; i++) *(u32x4 *)(slice + kc_chunk_offset(8 * i + lrow, lchunk, ROW)) = b[i];
+#pragma unroll
+    for (int i = 0; i < LA; i++) *(u32x4 *)(sa + kc_chunk_offset(8 * i + lrow, lchunk, ROW)) = a[i];
+    wave_lds_order();
+    if constexpr (!LAST) load(kb + waves);
     v8i32 fa[RB], fb[NT];
 #pragma unroll
-    for (int t = 0; t < NT; t++) fb[t] = frag(cur.b[t]);
+    for (int i = 0; i < RB; i++) fa[i] = frag(sa, AR >= 16 ? 16 * i + c : c & (AR - 1));
 #pragma unroll
-    for (int i = 0; i < RB; i++) fa[i] = frag(cur.a[i]);
-    mfma_e4m3_as_bf16<16>(acc, fa, fb);   // HBM-bound: the exact form costs nothing
-    cur = nxt;
+    for (int t = 0; t < NT; t++) fb[t] = frag(slice, 16 * t + c);
+    mfma_e4m3_as_bf16<16>(acc, fa, fb);                 // HBM-bound: the exact form costs nothing
+  };
+  if (wave < blocks) {
+    int kb = wave;
+    load(kb);
+    for (; kb + waves < blocks; kb += waves) block(kb, std::false_type{});
+    block(kb, std::true_type{});
   }
 
-  reduce_rows<RB, NT>(acc, red, waves, wave, lane, [&](int dm, int dn, float v) {
+  __syncthreads();                                      // the partial sums take the slices' place
+  reduce_rows<RB, NT>(acc, (float *)smem, waves, wave, lane, [&](int dm, int dn, float v) {
     const int m = m0 + dm, n = n0 + dn;
     if (m < M && n < N) store_rows<OUT>(C, (int64_t)m * ldc + n, scale_entry(v, m, n, M, N, sc));
   });
@@ -143,8 +178,8 @@ __global__ __launch_bounds__(64 / (RB * NT) >= 16 ? 1024 : 64 * (64 / (RB * NT))
 //
 // C[m][n] = sum_k a(m,k) * S[k / group][n] * (q(k,n) - z[k / group][n]).
 //
-// Weight n's row holds two 4-bit values a byte, even k in the low half, so a
-// lane's 16 bytes are 32 consecutive k.
+// Weight n's row holds two 4-bit values a byte, even k in the low half, so the
+// 16 bytes that a lane reads of its column are 32 consecutive k.
 //  * k across lanes.  A lane's 32 k would put the four 16-lane groups of one
 //    MFMA into four different scale groups when a group is 32 long.  Four
 //    permlane swaps transpose the 4 x 4 dwords of the lane groups (row i of
@@ -195,13 +230,13 @@ __device__ __forceinline__ v8i16 w4_unpack(uint32_t w) {
 }
 
 // Eight activations in the same order of pairs.
-__device__ __forceinline__ v8i16 w4_pairs(u32x4 a) {
+__device__ __forceinline__ u32x4 w4_pairs(u32x4 a) {
   u32x4 f;
   f[0] = __builtin_amdgcn_perm(a[2], a[0], 0x05040100u);
   f[1] = __builtin_amdgcn_perm(a[2], a[0], 0x07060302u);
   f[2] = __builtin_amdgcn_perm(a[3], a[1], 0x05040100u);
   f[3] = __builtin_amdgcn_perm(a[3], a[1], 0x07060302u);
-  return __builtin_bit_cast(v8i16, f);
+  return f;
 }
 
 // Transposes the dwords of the four 16-lane groups: dword j of group i <->
@@ -240,12 +275,44 @@ __device__ __forceinline__ float w4_entry(const W4Args &p, int m, int n) {
   return v;
 }
 
-// GS: k steps of 32 in a scale group (4 stands for every group of 128 or more).
-template <int IN, int RB, int NT, int GS>
-__global__ __launch_bounds__(64 / (RB * NT) >= 16 ? 1024 : 64 * (64 / (RB * NT))) void lds_gemm_w4_kernel(
-    const W4Args p) {
-  constexpr int NG = 4 / GS;             // scale groups in a block
-  extern __shared__ float red[];
+// The dword of lane 16 t + c, for every t, in every lane (c = lane & 15): rows
+// of 16 lanes copied over the others by permlane swaps.
+template <int NT>
+__device__ __forceinline__ void spread_rows(uint32_t (&out)[NT], uint32_t v) {
+  if constexpr (NT == 1) {
+    out[0] = v;
+  } else {
+    const auto x = __builtin_amdgcn_permlane16_swap(v, v, false, false);   // rows 0 0 2 2 and 1 1 3 3
+    if constexpr (NT == 2) {
+      out[0] = x[0];
+      out[1] = x[1];
+    } else {
+      const auto y = __builtin_amdgcn_permlane32_swap(x[0], x[0], false, false);
+      const auto z = __builtin_amdgcn_permlane32_swap(x[1], x[1], false, false);
+      out[0] = y[0];
+      out[1] = z[0];
+      out[2] = y[1];
+      out[3] = z[1];
+    }
+  }
+}
+
+// AR (4, 16, 32, 48 or 64): rows of A that are loaded; GS: k steps of 32 in a scale
+// group (4 stands for every group of 128 or more).
+template <int AR, int NT>
+struct RowsW4 {
+  static constexpr int RB = AR <= 16 ? 1 : AR / 16;
+  static constexpr int SLICE = rows_slice_bytes(AR, 2, 16 * NT, 4);
+  static constexpr int MAX_WAVES = rows_max_waves(RB, NT, SLICE);
+};
+
+template <int IN, int AR, int NT, int GS>
+__global__ __launch_bounds__((64 * RowsW4<AR, NT>::MAX_WAVES)) void lds_gemm_w4_kernel(const W4Args p) {
+  using T = RowsW4<AR, NT>;
+  constexpr int RB = T::RB, LA = AR / 4;                // loads of A: 4 rows x 256 bytes, of B: 16 rows x 64
+  constexpr int AROW = 2 * kRowsBlockK, BROW = kRowsBlockK / 2;
+  constexpr int NG = 4 / GS;                            // scale groups in a block
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   const int M = p.M, N = p.N, K = p.K;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -253,16 +320,32 @@ __global__ __launch_bounds__(64 / (RB * NT) >= 16 ? 1024 : 64 * (64 / (RB * NT))
   const int m0 = (id % p.tiles_m) * 16 * RB, n0 = (id / p.tiles_m) * 16 * NT;
 
   // Rows and columns past the end read the last one; their sums are not stored.
-  const uint16_t *arow[RB];
-  const uint8_t *brow[NT];
-  int col[NT];
+  // 32-bit offsets from the tile's first row and column (the host bounds lda and ldb).
+  const char *abase = (const char *)(p.A + (int64_t)m0 * p.lda);
+  const uint8_t *bbase = p.B + (int64_t)n0 * p.ldb;
+  const uint32_t lda = (uint32_t)(2 * p.lda), ldb = (uint32_t)p.ldb;
+  const uint32_t amax = (uint32_t)min(M - 1 - m0, 63) * lda, bmax = (uint32_t)min(N - 1 - n0, 63) * ldb;
+  const uint32_t scol = (uint32_t)min(n0 + (lane & (16 * NT - 1)), N - 1);   // whose scale this lane loads
+  char *slice = smem + wave * T::SLICE, *sa = slice + NT * 1024;
+
+  u32x4 a[LA], b[NT];
+  uint32_t sz[NG];                       // scale | zero point << 16 of column scol
+  auto load = [&](int kb) {
+    const int kbl = kb * kRowsBlockK + 32 * (lane & 3), kal = kb * kRowsBlockK + 8 * c;
+    // past K: the row's start, whose k steps are skipped
+    const uint32_t ob = kbl < K ? (uint32_t)kbl / 2 : 0, oa = kal < K ? (uint32_t)kal * 2 : 0;
 #pragma unroll
-  for (int i = 0; i < RB; i++) arow[i] = p.A + (int64_t)min(m0 + 16 * i + c, M - 1) * p.lda + 8 * g;
+    for (int t = 0; t < NT; t++)
+      b[t] = *(const u32x4 *)(bbase + (min((uint32_t)(16 * t + (lane >> 2)) * ldb, bmax) + ob));
 #pragma unroll
-  for (int t = 0; t < NT; t++) {
-    col[t] = min(n0 + 16 * t + c, N - 1);
-    brow[t] = p.B + (int64_t)col[t] * p.ldb;
-  }
+    for (int i = 0; i < NG; i++) {
+      const int64_t gi = min((kb * kRowsBlockK + 32 * GS * i) >> p.gshift, p.G - 1);
+      const uint32_t z = p.Z ? p.Z[gi * p.ldz + scol] : 8u;
+      sz[i] = p.S[gi * p.lds + scol] | z << 16;
+    }
+#pragma unroll
+    for (int i = 0; i < LA; i++) a[i] = *(const u32x4 *)(abase + (min((uint32_t)(4 * i + g) * lda, amax) + oa));
+  };
 
   v4f32 acc[RB][NT];
 #pragma unroll
@@ -270,46 +353,35 @@ __global__ __launch_bounds__(64 / (RB * NT) >= 16 ? 1024 : 64 * (64 / (RB * NT))
 #pragma unroll
     for (int t = 0; t < NT; t++) acc[i][t] = v4f32{0.f, 0.f, 0.f, 0.f};
 
-  struct Block {
-    u32x4 b[NT];
-    u32x4 a[RB][4];
-    uint16_t s[NT][NG];
-    uint8_t z[NT][NG];
-  };
-  auto load = [&](Block &f, int kb) {
-    const int k0 = kb * kRowsBlockK;
-    const int kl = k0 + 32 * g;
-    const int ob = kl < K ? kl / 2 : 0;  // past K: any weights, their k steps are skipped
-#pragma unroll
-    for (int t = 0; t < NT; t++) f.b[t] = *(const u32x4 *)(brow[t] + ob);
-#pragma unroll
-    for (int i = 0; i < NG; i++) {
-      const int64_t gi = min((k0 + 32 * GS * i) >> p.gshift, p.G - 1);
-#pragma unroll
-      for (int t = 0; t < NT; t++) {
-        f.s[t][i] = p.S[gi * p.lds + col[t]];
-        f.z[t][i] = p.Z ? p.Z[gi * p.ldz + col[t]] : (uint8_t)8;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int k = k0 + 32 * j < K ? k0 + 32 * j : 0;
-#pragma unroll
-      for (int i = 0; i < RB; i++) f.a[i][j] = *(const u32x4 *)(arow[i] + k);
-    }
-  };
-
   const v8i16 ones = __builtin_bit_cast(v8i16, u32x4{W4<IN>::ONES, W4<IN>::ONES, W4<IN>::ONES, W4<IN>::ONES});
   const int blocks = (K + kRowsBlockK - 1) / kRowsBlockK;
-  Block cur;
-  if (wave < blocks) load(cur, wave);
-  for (int kb = wave; kb < blocks; kb += waves) {
-    Block nxt;
-    if (kb + waves < blocks) load(nxt, kb + waves);
-    const int left = K - kb * kRowsBlockK;          // k of this block that exist
+  // One block; LAST: this wave's last one, which may be cut short by K.
+  auto block = [&](int kb, auto last) {
+    constexpr bool LAST = decltype(last)::value;
+    const int left = LAST ? K - kb * kRowsBlockK : kRowsBlockK;   // k of this block that exist
+    wave_lds_order();
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+      *(u32x4 *)(slice + kc_chunk_offset(16 * t + (lane >> 2), lane & 3, BROW)) = b[t];
+#pragma unroll
+    for (int i = 0; i < LA; i++) *(u32x4 *)(sa + kc_chunk_offset(4 * i + g, c, AROW)) = w4_pairs(a[i]);
+    wave_lds_order();
+    float s[NG][NT], z[NG][NT];
+#pragma unroll
+    for (int i = 0; i < NG; i++) {
+      uint32_t v[NT];
+      spread_rows<NT>(v, sz[i]);
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        s[i][t] = to_f32<IN>((uint16_t)v[t]);
+        z[i][t] = 16.f + (float)(v[t] >> 16);
+      }
+    }
+    if constexpr (!LAST) load(kb + waves);
     u32x4 w[NT];
 #pragma unroll
-    for (int t = 0; t < NT; t++) w[t] = lane_group_transpose(cur.b[t]);
+    for (int t = 0; t < NT; t++)
+      w[t] = lane_group_transpose(*(const u32x4 *)(slice + kc_chunk_offset(16 * t + c, g, BROW)));
 #pragma unroll
     for (int gi = 0; gi < NG; gi++) {
       v4f32 sum[RB], part[RB][NT];
@@ -325,7 +397,8 @@ __global__ __launch_bounds__(64 / (RB * NT) >= 16 ? 1024 : 64 * (64 / (RB * NT))
           v8i16 fa[RB];
 #pragma unroll
           for (int i = 0; i < RB; i++) {
-            fa[i] = w4_pairs(cur.a[i][j]);
+            const int row = AR >= 16 ? 16 * i + c : c & (AR - 1);
+            fa[i] = *(const v8i16 *)(sa + kc_chunk_offset(row, 4 * j + g, AROW));
             sum[i] = mfma_16x16x32<IN>(fa[i], ones, sum[i]);
           }
 #pragma unroll
@@ -338,20 +411,23 @@ __global__ __launch_bounds__(64 / (RB * NT) >= 16 ? 1024 : 64 * (64 / (RB * NT))
       }
       if (32 * gi * GS < left) {
 #pragma unroll
-        for (int t = 0; t < NT; t++) {
-          const float s = to_f32<IN>(cur.s[t][gi]);
-          const float z = 16.f + (float)cur.z[t][gi];
+        for (int t = 0; t < NT; t++)
 #pragma unroll
           for (int i = 0; i < RB; i++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) acc[i][t][r] += s * (part[i][t][r] - z * sum[i][r]);
-        }
+            for (int r = 0; r < 4; r++) acc[i][t][r] += s[gi][t] * (part[i][t][r] - z[gi][t] * sum[i][r]);
       }
     }
-    cur = nxt;
+  };
+  if (wave < blocks) {
+    int kb = wave;
+    load(kb);
+    for (; kb + waves < blocks; kb += waves) block(kb, std::false_type{});
+    block(kb, std::true_type{});
   }
 
-  reduce_rows<RB, NT>(acc, red, waves, wave, lane, [&](int dm, int dn, float v) {
+  __syncthreads();                       // the partial sums take the slices' place
+  reduce_rows<RB, NT>(acc, (float *)smem, waves, wave, lane, [&](int dm, int dn, float v) {
     const int m = m0 + dm, n = n0 + dn;
     if (m >= M || n >= N) return;
     if (!__builtin_isfinite(v)) v = w4_entry<IN>(p, m, n);

@@ -24,47 +24,50 @@ static hipError_t launch_scaled(const Args &a, int la, int lb, int dtype, hipStr
   }
 }
 
-template <int RB, int NT, int OUT>
-static hipError_t launch_rows(const Args &a, int waves, hipStream_t stream, RowColScale sc) {
+template <int AR, int NT, int OUT>
+static hipError_t launch_rows(const Args &a, hipStream_t stream, RowColScale sc) {
+  using T = RowsE4M3<AR, NT>;
+  int waves = 1;
+  while (2 * waves <= T::MAX_WAVES && 2 * waves * kRowsBlockK <= a.K) waves *= 2;
   const char *A = (const char *)a.A, *B = (const char *)a.B;
   void *C = a.C;
   int M = a.M, N = a.N, K = a.K;
-  int64_t lda = a.lda, ldb = a.ldb, ldc = a.ldc;
-  int tiles_m = (int)ceil_div(a.M, 16 * RB);
+  uint32_t lda = (uint32_t)a.lda, ldb = (uint32_t)a.ldb;
+  int64_t ldc = a.ldc;
+  int tiles_m = (int)ceil_div(a.M, 16 * T::RB);
   const int64_t tiles = tiles_m * ceil_div(a.N, 16 * NT);
   void *params[] = {&A, &B, &C, &M, &N, &K, &lda, &ldb, &ldc, &tiles_m, &sc};
-  return hipLaunchKernel((const void *)lds_gemm_rows_e4m3_kernel<RB, NT, OUT>, dim3((unsigned)tiles),
-                         dim3(64u * waves), params, (size_t)waves * RB * NT * 1024, stream);
+  return hipLaunchKernel((const void *)lds_gemm_rows_e4m3_kernel<AR, NT, OUT>, dim3((unsigned)tiles),
+                         dim3(64u * waves), params,
+                         (size_t)waves * (T::SLICE > 1024 * T::RB * NT ? T::SLICE : 1024 * T::RB * NT), stream);
 }
 
-template <int RB, int NT>
-static hipError_t launch_rows_out(const Args &a, int waves, int dtype, hipStream_t s, const RowColScale &sc) {
+template <int AR, int NT>
+static hipError_t launch_rows_out(const Args &a, int dtype, hipStream_t s, const RowColScale &sc) {
   switch (dtype) {
-    case GEMM_E4M3_F32: return launch_rows<RB, NT, OUT_F32>(a, waves, s, sc);
-    case GEMM_E4M3_BF16: return launch_rows<RB, NT, OUT_BF16>(a, waves, s, sc);
-    default: return launch_rows<RB, NT, OUT_F16>(a, waves, s, sc);
+    case GEMM_E4M3_F32: return launch_rows<AR, NT, OUT_F32>(a, s, sc);
+    case GEMM_E4M3_BF16: return launch_rows<AR, NT, OUT_BF16>(a, s, sc);
+    default: return launch_rows<AR, NT, OUT_F16>(a, s, sc);
   }
 }
 
 // Column blocks by N: the widest tile that still makes a workgroup for every
-// CU; then as many waves as K has blocks for, up to 16 and to 64 KiB of
-// partial sums.
-template <int RB>
+// CU; then as many waves as K has blocks for.
+template <int AR>
 static hipError_t dispatch_rows(const Args &a, int dtype, hipStream_t s, const RowColScale &sc) {
-  const int64_t rows = ceil_div(a.M, 16 * RB);
-  const int nt = rows * ceil_div(a.N, 64) >= 256 ? 4 : rows * ceil_div(a.N, 32) >= 256 ? 2 : 1;
-  int waves = 1;
-  while (waves < 16 && 2 * waves * RB * nt <= 64 && 2 * waves * kRowsBlockK <= a.K) waves *= 2;
-  if (nt == 4) return launch_rows_out<RB, 4>(a, waves, dtype, s, sc);
-  if (nt == 2) return launch_rows_out<RB, 2>(a, waves, dtype, s, sc);
-  return launch_rows_out<RB, 1>(a, waves, dtype, s, sc);
+  const int nt = ceil_div(a.N, 64) >= 256 ? 4 : ceil_div(a.N, 32) >= 256 ? 2 : 1;
+  if (nt == 4) return launch_rows_out<AR, 4>(a, dtype, s, sc);
+  if (nt == 2) return launch_rows_out<AR, 2>(a, dtype, s, sc);
+  return launch_rows_out<AR, 1>(a, dtype, s, sc);
 }
 
 // The shape classes of gemm_run's E4M3 products; at most 32 rows with both
 // operands K-contiguous take the few-rows kernel.
 static hipError_t dispatch_scaled(const Args &a, int la, int lb, int dtype, hipStream_t s, const RowColScale &sc) {
-  if (a.M <= 16 && la == KC && lb == KC) return dispatch_rows<1>(a, dtype, s, sc);
-  if (a.M <= 32 && la == KC && lb == KC) return dispatch_rows<2>(a, dtype, s, sc);
+  if (a.M <= 32 && la == KC && lb == KC) {
+    if (a.M <= 8) return dispatch_rows<8>(a, dtype, s, sc);
+    return a.M <= 16 ? dispatch_rows<16>(a, dtype, s, sc) : dispatch_rows<32>(a, dtype, s, sc);
+  }
   if (a.M <= 32) return launch_scaled<SkinnyStream8, SKINNY, IN_E4M3_AS_BF16>(a, la, lb, dtype, s, sc);
   if (ceil_div(a.M, 256) * ceil_div(a.N, 256) >= 256)
     return launch_scaled<PingPong8, PINGPONG>(a, la, lb, dtype, s, sc);

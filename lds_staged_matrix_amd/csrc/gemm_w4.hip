@@ -9,42 +9,44 @@
 
 namespace lsm {
 
-template <int IN, int RB, int NT, int GS>
+template <int IN, int AR, int NT, int GS>
 static hipError_t launch_w4(const W4Args &p, int waves, hipStream_t stream) {
+  using T = RowsW4<AR, NT>;
   W4Args a = p;
-  a.tiles_m = (int)ceil_div(p.M, 16 * RB);
+  a.tiles_m = (int)ceil_div(p.M, 16 * T::RB);
   const int64_t tiles = a.tiles_m * ceil_div(p.N, 16 * NT);
   void *params[] = {&a};
-  return hipLaunchKernel((const void *)lds_gemm_w4_kernel<IN, RB, NT, GS>, dim3((unsigned)tiles),
-                         dim3(64u * waves), params, (size_t)waves * RB * NT * 1024, stream);
+  return hipLaunchKernel((const void *)lds_gemm_w4_kernel<IN, AR, NT, GS>, dim3((unsigned)tiles), dim3(64u * waves),
+                         params, (size_t)waves * (T::SLICE > 1024 * T::RB * NT ? T::SLICE : 1024 * T::RB * NT), stream);
 }
 
-template <int IN, int RB, int NT>
-static hipError_t launch_w4_group(const W4Args &p, int waves, hipStream_t s) {
-  if (p.gshift == 5) return launch_w4<IN, RB, NT, 1>(p, waves, s);
-  if (p.gshift == 6) return launch_w4<IN, RB, NT, 2>(p, waves, s);
-  return launch_w4<IN, RB, NT, 4>(p, waves, s);
+template <int IN, int AR, int NT>
+static hipError_t launch_w4_group(const W4Args &p, hipStream_t s) {
+  int waves = 1;
+  while (2 * waves <= RowsW4<AR, NT>::MAX_WAVES && 2 * waves * kRowsBlockK <= p.K) waves *= 2;
+  if (p.gshift == 5) return launch_w4<IN, AR, NT, 1>(p, waves, s);
+  if (p.gshift == 6) return launch_w4<IN, AR, NT, 2>(p, waves, s);
+  return launch_w4<IN, AR, NT, 4>(p, waves, s);
 }
 
 // Row blocks by M, column blocks by N: the widest tile that still makes a
-// workgroup for every CU; then as many waves as K has blocks for, up to 16 and
-// to 64 KiB of partial sums.
-template <int IN, int RB>
+// workgroup for every CU; then as many waves as K has blocks for.
+template <int IN, int AR>
 static hipError_t launch_w4_rows(const W4Args &p, hipStream_t s) {
-  const int64_t rows = ceil_div(p.M, 16 * RB);
+  const int64_t rows = ceil_div(p.M, AR < 16 ? 16 : AR);
   const int nt = rows * ceil_div(p.N, 64) >= 256 ? 4 : rows * ceil_div(p.N, 32) >= 256 ? 2 : 1;
-  int waves = 1;
-  while (waves < 16 && 2 * waves * RB * nt <= 64 && 2 * waves * kRowsBlockK <= p.K) waves *= 2;
-  if (nt == 4) return launch_w4_group<IN, RB, 4>(p, waves, s);
-  if (nt == 2) return launch_w4_group<IN, RB, 2>(p, waves, s);
-  return launch_w4_group<IN, RB, 1>(p, waves, s);
+  if (nt == 4) return launch_w4_group<IN, AR, 4>(p, s);
+  if (nt == 2) return launch_w4_group<IN, AR, 2>(p, s);
+  return launch_w4_group<IN, AR, 1>(p, s);
 }
 
 template <int IN>
 static hipError_t dispatch_w4(const W4Args &p, hipStream_t s) {
-  if (p.M <= 16) return launch_w4_rows<IN, 1>(p, s);
-  if (p.M <= 32) return launch_w4_rows<IN, 2>(p, s);
-  return launch_w4_rows<IN, 4>(p, s);
+  if (p.M <= 4) return launch_w4_rows<IN, 4>(p, s);
+  if (p.M <= 16) return launch_w4_rows<IN, 16>(p, s);
+  if (p.M <= 32) return launch_w4_rows<IN, 32>(p, s);
+  if (p.M <= 48 && p.M > 32) return launch_w4_rows<IN, 48>(p, s);
+  return launch_w4_rows<IN, 64>(p, s);
 }
 
 }  // namespace lsm
@@ -65,6 +67,8 @@ extern "C" int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const 
   if (lda >= kMaxLd || ldb >= kMaxLd || lds >= kMaxLd || ldz >= kMaxLd || ldc >= kMaxLd)
     return GEMM_ERR_UNSUPPORTED;
   // groups of a power of two of at least 32, and whole 32s of K
+  // 32-bit offsets inside a tile of 64 rows or columns
+  if (K > 0 && (lda >= ((int64_t)1 << 24) || ldb >= ((int64_t)1 << 25))) return GEMM_ERR_UNSUPPORTED;
   if (group < 32 || (group & (group - 1)) || group > kMaxDim || K % 32) return GEMM_ERR_UNSUPPORTED;
   if (ceil_div(M, 16) * ceil_div(N, 16) >= ((int64_t)1 << 31)) return GEMM_ERR_UNSUPPORTED;
   if ((uintptr_t)C & (out_f32 ? 3 : 1)) return GEMM_ERR_UNSUPPORTED;

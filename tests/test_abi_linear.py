@@ -103,6 +103,8 @@ W4_CASES = [
     (dict(S=addr(2) + 2), VALID), (dict(Z=addr(3) + 1), VALID), (dict(C=addr(4) + 2), UNSUPPORTED),
     (dict(C=addr(4) + 2, dtype=lsm.GEMM_BF16_BF16), VALID),
     (dict(M=1 << 30), UNSUPPORTED), (dict(lda=1 << 40), UNSUPPORTED), (dict(ldb=1 << 40), UNSUPPORTED),
+    (dict(lda=1 << 24), UNSUPPORTED), (dict(lda=(1 << 24) - 8, A=1 << 40), VALID), (dict(ldb=1 << 25), UNSUPPORTED),
+    (dict(ldb=(1 << 25) - 32, B=1 << 40), VALID),
     (dict(lds=1 << 40), UNSUPPORTED), (dict(ldz=1 << 40), UNSUPPORTED), (dict(ldc=1 << 40), UNSUPPORTED),
     (dict(M=(1 << 30) - 1, N=(1 << 30) - 1, lds=1 << 30, ldz=1 << 30, ldc=1 << 30), UNSUPPORTED),
     (dict(M=1 << 29, ldc=(1 << 39)), UNSUPPORTED),
