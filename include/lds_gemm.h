@@ -173,8 +173,7 @@ int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const void *S,
  *   ldx, ldy >= N, ldr >= N with R, ldh >= N with H; each < 2^40.
  *   eps >= 0;  M == 0 or N == 0 is a no-op.
  * H and a 16-bit Y may each stand in the place of X or of R (same address and
- * leading dimension); no other overlap with an output is allowed.  Rows that
- * start on 16 bytes (8 for E4M3) take wide accesses. */
+ * leading dimension); no other overlap with an output is allowed. */
 int gemm_rmsnorm_run(gemm_handle_t h, const void *X, const void *R, const void *W,
                      void *H, void *Y, float *S,
                      int64_t M, int64_t N,

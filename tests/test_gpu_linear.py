@@ -121,7 +121,7 @@ def test_norm_sizes(M, N, kind, out):
         check_norm(M, N, kind, out, run_norm(M, N, kind, out, residual, keep_h=residual))
 
 
-@pytest.mark.parametrize("M,N", [(3, 1), (5, 63), (2, 513), (3, 1151), (2, 5000), (1, 9001), (2, 17001)])
+@pytest.mark.parametrize("M,N", [(3, 1), (5, 63), (2, 513), (3, 1151), (2, 5000), (1, 9001), (2, 17001), (2, 33003)])
 @pytest.mark.parametrize("out", ["f16", "e4m3"])
 @pytest.mark.parametrize("pad,shift", [(1, 0), (8, 1)])
 def test_norm_unaligned_rows(M, N, out, pad, shift):
@@ -169,7 +169,7 @@ def test_norm_zero_eps():
     check_norm(2, 96, "f16", "f16", (h, y, None, Y, None))
 
 
-@pytest.mark.parametrize("N", [520, 4096, 33000])
+@pytest.mark.parametrize("N", [5, 9, 500, 520, 1151, 4096, 9001, 33000, 33003])
 @pytest.mark.parametrize("into", ["X", "R"])
 def test_norm_in_place(N, into):
     """H in the residual's or the input's place, Y in the other's."""
