@@ -92,6 +92,14 @@ def _ptr(x):
         return int(x)
 
 
+def _ptrs(*xs):
+    """_ptr of each, in one go for what torch programs pass."""
+    try:
+        return [None if x is None else x.data_ptr() for x in xs]
+    except AttributeError:
+        return [_ptr(x) for x in xs]
+
+
 def _int(x, bits, name):
     """x as a Python int that fits the C ABI's signed `bits`-bit parameter.
     ctypes would silently keep only the low bits of a larger value."""
@@ -153,21 +161,21 @@ def gemm_scaled_run(h, A, B, C, SA, SB, M, N, K, lda, ldb, ldc, incA, incB, layo
                     stream=None) -> int:
     """Enqueue C <- diag(SA) A B diag(SB) for E4M3 operands; returns the gemm_status code."""
     return load_library().gemm_scaled_run(
-        h, _ptr(A), _ptr(B), _ptr(C), _ptr(SA), _ptr(SB),
+        h, *_ptrs(A, B, C, SA, SB),
         *_SCALED(M, N, K, lda, ldb, ldc, incA, incB, layoutA, layoutB, dtype), _stream(stream))
 
 
 def gemm_w4_run(h, A, B, S, Z, C, M, N, K, group, lda, ldb, lds, ldz, ldc, dtype, stream=None) -> int:
     """Enqueue the product of 16-bit rows with 4-bit weights; returns the gemm_status code."""
-    return load_library().gemm_w4_run(h, _ptr(A), _ptr(B), _ptr(S), _ptr(Z), _ptr(C),
+    return load_library().gemm_w4_run(h, *_ptrs(A, B, S, Z, C),
                                       *_W4(M, N, K, group, lda, ldb, lds, ldz, ldc, dtype), _stream(stream))
 
 
 def gemm_rmsnorm_run(h, X, R, W, H, Y, S, M, N, ldx, ldr, ldh, ldy, eps, dtype, stream=None) -> int:
     """Enqueue the RMS norm of X (+ R); returns the gemm_status code."""
     M, N, ldx, ldr, ldh, ldy, dtype = _NORM(M, N, ldx, ldr, ldh, ldy, dtype)
-    return load_library().gemm_rmsnorm_run(h, _ptr(X), _ptr(R), _ptr(W), _ptr(H), _ptr(Y), _ptr(S), M, N, ldx, ldr,
-                                           ldh, ldy, eps, dtype, _stream(stream))
+    return load_library().gemm_rmsnorm_run(h, *_ptrs(X, R, W, H, Y, S), M, N, ldx, ldr, ldh, ldy, eps, dtype,
+                                           _stream(stream))
 
 
 def gemm_destroy(h) -> int:

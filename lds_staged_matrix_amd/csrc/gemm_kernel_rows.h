@@ -7,7 +7,7 @@
 //  * A workgroup owns 16 * NT columns and 16 * RB rows of C; its waves split K
 //    among them in blocks of 128, interleaved, so that the waves of a workgroup
 //    together read whole lines of each weight row.  Splitting K inside the
-//    workgroup is what puts 16 waves on every CU when N is a few thousand; the
+//    workgroup is what fills every CU when N is a few thousand; the
 //    partial sums meet in LDS and are added in wave order, so a result does not
 //    depend on timing.
 //  * Loads take a block row by row: the lanes of a quarter wave read 256 (64,
@@ -28,24 +28,41 @@
 #include <type_traits>
 
 #include "gemm_common.h"
+#include "gemm_kernel_dma.h"
 
 namespace lsm {
 
 constexpr int kRowsBlockK = 128;         // k of one load block
 
-// The most waves of a workgroup: 128 registers a lane for 16 waves, 256 for
-// eight, and 160 KiB of LDS for the waves' slices (which the partial sums reuse).
-constexpr int rows_max_waves(int rb, int nt, int slice) {
-  int w = rb >= 3 || rb * nt >= 8 ? 8 : 16;
-  while (w * slice > 160 * 1024) w /= 2;
-  return w;
-}
+constexpr int kRowsMaxWaves = 8;         // of a workgroup
 
 // Orders a wave's own LDS writes and reads, lane against lane, in the compiler
 // (the hardware runs them in order).
 __device__ __forceinline__ void wave_lds_order() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_wave_barrier();
+}
+
+// 16 bytes at base + voff + soff: voff one register a lane, constant over the K
+// loop, soff uniform.  (As a flat address the compiler keeps base + voff in two
+// registers and adds to them in every round.)  The record count is no bound
+// here: the callers' offsets stay inside the operand.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, ~0u, kBufferWord3);
+}
+__device__ __forceinline__ u32x4 rows_load(__amdgpu_buffer_rsrc_t rs, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, voff, soff, 0));
+}
+
+// Where in K a workgroup starts, in blocks of `full`: each XCD at an eighth of
+// its own.  Workgroups that start together everywhere ask for the same
+// kilobyte of rows that lie a power of two apart, which a part of the HBM
+// channels holds: 1 x 16384 x 8192 E4M3 took 31.4 us, with the eighths 25.0
+// (5.4 TB/s); 4 bits, 1 x 28672 x 8192, 31.4 and 28.2 us.  Inside an XCD all start
+// together, so that the activations they share stay in its L2 (a start of
+// each tile's own took 16.4 instead of 11.8 us for 1 x 8192 x 8192 E4M3).
+__device__ __forceinline__ int rows_start(int full) {
+  return (int)((uint32_t)(blockIdx.x & 7) * (uint32_t)full >> 3);
 }
 
 // LDS bytes of one wave's slice: `arows` rows of A and `bcols` columns of B, one block of each.
@@ -84,17 +101,17 @@ __device__ __forceinline__ void store_rows(void *C, int64_t idx, float v) {
 // ------------------------------------------------------------------- E4M3
 //
 // C[m][n] = sum_k a(m,k) b(k,n) * sc.a[m] * sc.b[n], both operands
-// K-contiguous, K a multiple of 16.  AR (8, 16 or 32): rows of A that are
-// loaded; RB = 1 of 16 rows or 2.
+// K-contiguous, K a multiple of 16.  AR (8, 16, 32, 48 or 64): rows of A that
+// are loaded.
 template <int AR, int NT>
 struct RowsE4M3 {
   static constexpr int RB = AR <= 16 ? 1 : AR / 16;
   static constexpr int SLICE = rows_slice_bytes(AR, 1, 16 * NT, 8);
-  static constexpr int MAX_WAVES = rows_max_waves(RB, NT, SLICE);
+  static constexpr int WAVES_PER_SIMD = RB <= 2 ? 4 : 2;   // 128 registers a lane, or 256
 };
 
 template <int AR, int NT, int OUT>
-__global__ __launch_bounds__((64 * RowsE4M3<AR, NT>::MAX_WAVES)) void lds_gemm_rows_e4m3_kernel(
+__global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsE4M3<AR, NT>::WAVES_PER_SIMD)) void lds_gemm_rows_e4m3_kernel(
     const char *__restrict__ A, const char *__restrict__ B, void *__restrict__ C, int M, int N, int K,
     uint32_t lda, uint32_t ldb, int64_t ldc, int tiles_m, RowColScale sc) {
   using T = RowsE4M3<AR, NT>;
@@ -107,20 +124,34 @@ __global__ __launch_bounds__((64 * RowsE4M3<AR, NT>::MAX_WAVES)) void lds_gemm_r
   const int m0 = (id % tiles_m) * 16 * RB, n0 = (id / tiles_m) * 16 * NT;
 
   // Rows and columns past the end read the last one; their sums are not stored.
-  const char *abase = A + (int64_t)m0 * lda, *bbase = B + (int64_t)n0 * ldb;
-  const uint32_t amax = (uint32_t)(M - 1 - m0) * lda, bmax = (uint32_t)(N - 1 - n0) * ldb;
+  const auto rsa = rows_rsrc(A + (int64_t)m0 * lda), rsb = rows_rsrc(B + (int64_t)n0 * ldb);
   const int lrow = lane >> 3, lchunk = lane & 7;        // of a load
+  uint32_t aoff[LA], boff[LB];
+#pragma unroll
+  for (int i = 0; i < LA; i++) aoff[i] = (uint32_t)min(8 * i + lrow, M - 1 - m0) * lda + 16u * lchunk;
+#pragma unroll
+  for (int i = 0; i < LB; i++) boff[i] = (uint32_t)min(8 * i + lrow, N - 1 - n0) * ldb + 16u * lchunk;
   char *slice = smem + wave * T::SLICE, *sa = slice + LB * 1024;
 
   u32x4 a[LA], b[LB];
-  auto load = [&](int kb) {
-    const int k = kb * kRowsBlockK + 16 * lchunk;
-    // a chunk at k >= K reads the row's start and counts as zero below
-    const uint32_t o = k < K ? (uint32_t)k : 0;
+  // PART: the block is cut short by K, and what lies behind K counts as zero.
+  auto load = [&](int kb, auto part) {
+    constexpr bool PART = decltype(part)::value;
+    const uint32_t k0 = kb * kRowsBlockK;
+    const bool past = PART && (int)(k0 + 16 * lchunk) >= K;
+    // past K: the row's start, whatever it holds, and then zeros
+    const uint32_t add = PART ? past ? 0u - 16u * lchunk : k0 : 0u;
+    const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < LB; i++) b[i] = *(const u32x4 *)(bbase + (min((uint32_t)(8 * i + lrow) * ldb, bmax) + o));
+    for (int i = 0; i < LB; i++) {
+      b[i] = rows_load(rsb, boff[i] + add, PART ? 0 : k0);
+      if (past) b[i] = zero;
+    }
 #pragma unroll
-    for (int i = 0; i < LA; i++) a[i] = *(const u32x4 *)(abase + (min((uint32_t)(8 * i + lrow) * lda, amax) + o));
+    for (int i = 0; i < LA; i++) {
+      a[i] = rows_load(rsa, aoff[i] + add, PART ? 0 : k0);
+      if (past) a[i] = zero;
+    }
   };
   // operand of row r (of a slice part): the 32 bytes at k = 32 g
   auto frag = [&](const char *part, int r) {
@@ -135,24 +166,15 @@ __global__ __launch_bounds__((64 * RowsE4M3<AR, NT>::MAX_WAVES)) void lds_gemm_r
 #pragma unroll
     for (int t = 0; t < NT; t++) acc[i][t] = v4f32{0.f, 0.f, 0.f, 0.f};
 
-  const int blocks = (K + kRowsBlockK - 1) / kRowsBlockK;
-  auto block = [&](int kb, auto last) {
-    constexpr bool LAST = decltype(last)::value;
-    if constexpr (LAST) {
-      if (kb * kRowsBlockK + 16 * lchunk >= K) {        // zeros on both sides: a NaN may stand at the row's start
-#pragma unroll
-        for (int i = 0; i < LB; i++) b[i] = u32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < LA; i++) a[i] = u32x4{0, 0, 0, 0};
-      }
-    }
+  // The products of the loaded block; next() issues the next one's loads.
+  auto block = [&](auto next) {
     wave_lds_order();
 #pragma unroll
     for (int i = 0; i < LB; i++) *(u32x4 *)(slice + kc_chunk_offset(8 * i + lrow, lchunk, ROW)) = b[i];
 #pragma unroll
     for (int i = 0; i < LA; i++) *(u32x4 *)(sa + kc_chunk_offset(8 * i + lrow, lchunk, ROW)) = a[i];
     wave_lds_order();
-    if constexpr (!LAST) load(kb + waves);
+    next();
     v8i32 fa[RB], fb[NT];
 #pragma unroll
     for (int i = 0; i < RB; i++) fa[i] = frag(sa, AR >= 16 ? 16 * i + c : c & (AR - 1));
@@ -160,11 +182,19 @@ __global__ __launch_bounds__((64 * RowsE4M3<AR, NT>::MAX_WAVES)) void lds_gemm_r
     for (int t = 0; t < NT; t++) fb[t] = frag(slice, 16 * t + c);
     mfma_e4m3_as_bf16<16>(acc, fa, fb);                 // HBM-bound: the exact form costs nothing
   };
-  if (wave < blocks) {
-    int kb = wave;
-    load(kb);
-    for (; kb + waves < blocks; kb += waves) block(kb, std::false_type{});
-    block(kb, std::true_type{});
+  // Whole blocks go round the waves; the last wave takes the cut one first.
+  const int full = K / kRowsBlockK, start = rows_start(full);
+  auto at = [&](int kb) { return kb + start < full ? kb + start : kb + start - full; };
+  const std::false_type whole{};
+  if (K % kRowsBlockK != 0 && wave == waves - 1) {
+    load(full, std::true_type{});
+    block([] {});
+  }
+  int kb = wave;
+  if (kb < full) {
+    load(at(kb), whole);
+    for (; kb + waves < full; kb += waves) block([&] { load(at(kb + waves), whole); });
+    block([] {});
   }
 
   __syncthreads();                                      // the partial sums take the slices' place
@@ -217,16 +247,23 @@ __device__ __forceinline__ float to_f32(uint16_t x) {
     return (float)__builtin_bit_cast(_Float16, x);
 }
 
-// Eight weights (one dword) as the pairs (16 + q_i, 16 + q_{i+4}).
+// Eight weights (one dword) as the pairs (16 + q_i, 16 + q_{i+4}): a shift and
+// one v_and_or_b32 a pair, with its two constants in registers (`mask`,
+// `base`: W4<IN>::MASK and BASE behind w4_constant).
 template <int IN>
-__device__ __forceinline__ v8i16 w4_unpack(uint32_t w) {
+__device__ __forceinline__ v8i16 w4_unpack(uint32_t w, uint32_t mask, uint32_t base) {
   u32x4 f;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     const int sh = 4 * i - W4<IN>::POS;
-    f[i] = ((sh < 0 ? w << -sh : w >> sh) & W4<IN>::MASK) | W4<IN>::BASE;
+    f[i] = ((sh < 0 ? w << -sh : w >> sh) & mask) | base;
   }
   return __builtin_bit_cast(v8i16, f);
+}
+
+__device__ __forceinline__ uint32_t w4_constant(uint32_t v) {
+  asm("" : "+v"(v));         // not folded into an and and an or with literals
+  return v;
 }
 
 // Eight activations in the same order of pairs.
@@ -253,11 +290,12 @@ struct W4Args {
   const uint16_t *A;
   const uint8_t *B;
   const uint16_t *S;
-  const uint8_t *Z;      // NULL: every zero point is 8
+  const uint8_t *Z;      // any readable row of N bytes where zmask is 0
   void *C;
   int M, N, K, G, gshift;             // K groups of 2^gshift
   int64_t lda, ldb, lds, ldz, ldc;    // ldb in bytes
   int tiles_m, out_f32;
+  uint32_t zmask, zadd;               // zero point = (byte & zmask) + zadd
 };
 
 // One entry, summed term by term in the order of k.
@@ -269,7 +307,7 @@ __device__ __forceinline__ float w4_entry(const W4Args &p, int m, int n) {
   for (int k = 0; k < p.K; k++) {
     const int64_t gi = k >> p.gshift;
     const int q = (b[k >> 1] >> (4 * (k & 1))) & 15;
-    const int z = p.Z ? p.Z[gi * p.ldz + n] : 8;
+    const int z = (int)((p.Z[gi * p.ldz + n] & p.zmask) + p.zadd);
     v += to_f32<IN>(a[k]) * ((float)(q - z) * to_f32<IN>(p.S[gi * p.lds + n]));
   }
   return v;
@@ -303,11 +341,11 @@ template <int AR, int NT>
 struct RowsW4 {
   static constexpr int RB = AR <= 16 ? 1 : AR / 16;
   static constexpr int SLICE = rows_slice_bytes(AR, 2, 16 * NT, 4);
-  static constexpr int MAX_WAVES = rows_max_waves(RB, NT, SLICE);
+  static constexpr int WAVES_PER_SIMD = RB == 1 ? 4 : 2;   // 128 registers a lane, or 256
 };
 
 template <int IN, int AR, int NT, int GS>
-__global__ __launch_bounds__((64 * RowsW4<AR, NT>::MAX_WAVES)) void lds_gemm_w4_kernel(const W4Args p) {
+__global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsW4<AR, NT>::WAVES_PER_SIMD)) void lds_gemm_w4_kernel(const W4Args p) {
   using T = RowsW4<AR, NT>;
   constexpr int RB = T::RB, LA = AR / 4;                // loads of A: 4 rows x 256 bytes, of B: 16 rows x 64
   constexpr int AROW = 2 * kRowsBlockK, BROW = kRowsBlockK / 2;
@@ -321,30 +359,45 @@ __global__ __launch_bounds__((64 * RowsW4<AR, NT>::MAX_WAVES)) void lds_gemm_w4_
 
   // Rows and columns past the end read the last one; their sums are not stored.
   // 32-bit offsets from the tile's first row and column (the host bounds lda and ldb).
-  const char *abase = (const char *)(p.A + (int64_t)m0 * p.lda);
-  const uint8_t *bbase = p.B + (int64_t)n0 * p.ldb;
-  const uint32_t lda = (uint32_t)(2 * p.lda), ldb = (uint32_t)p.ldb;
-  const uint32_t amax = (uint32_t)min(M - 1 - m0, 63) * lda, bmax = (uint32_t)min(N - 1 - n0, 63) * ldb;
+  const auto rsa = rows_rsrc(p.A + (int64_t)m0 * p.lda), rsb = rows_rsrc(p.B + (int64_t)n0 * p.ldb);
+  uint32_t aoff[LA], boff[NT];
+#pragma unroll
+  for (int i = 0; i < LA; i++) aoff[i] = (uint32_t)min(4 * i + g, M - 1 - m0) * (uint32_t)(2 * p.lda) + 16u * c;
+#pragma unroll
+  for (int t = 0; t < NT; t++)
+    boff[t] = (uint32_t)min(16 * t + (lane >> 2), N - 1 - n0) * (uint32_t)p.ldb + 16u * (lane & 3);
   const uint32_t scol = (uint32_t)min(n0 + (lane & (16 * NT - 1)), N - 1);   // whose scale this lane loads
   char *slice = smem + wave * T::SLICE, *sa = slice + NT * 1024;
 
   u32x4 a[LA], b[NT];
-  uint32_t sz[NG];                       // scale | zero point << 16 of column scol
-  auto load = [&](int kb) {
-    const int kbl = kb * kRowsBlockK + 32 * (lane & 3), kal = kb * kRowsBlockK + 8 * c;
-    // past K: the row's start, whose k steps are skipped
-    const uint32_t ob = kbl < K ? (uint32_t)kbl / 2 : 0, oa = kal < K ? (uint32_t)kal * 2 : 0;
+  uint16_t s16[NG];                      // scales and zero points of column scol
+  uint8_t z8[NG];
+  // Quarter `at` of the loads of block kb: the weights, scales and zero points
+  // come with the first, and a quarter of A with each.  PART: the block is cut
+  // short by K, and what lies behind K reads the row's start instead; the k
+  // steps of that are skipped.
+  auto load = [&](int kb, int at, auto part) {
+    constexpr bool PART = decltype(part)::value;
+    const int k0 = kb * kRowsBlockK;
+    if (at == 0) {
 #pragma unroll
-    for (int t = 0; t < NT; t++)
-      b[t] = *(const u32x4 *)(bbase + (min((uint32_t)(16 * t + (lane >> 2)) * ldb, bmax) + ob));
+      for (int t = 0; t < NT; t++)
+        b[t] = rows_load(rsb, PART && k0 + 32 * (lane & 3) >= K ? boff[t] - 16 * (lane & 3) : boff[t] + (PART ? k0 / 2 : 0),
+                         PART ? 0 : k0 / 2);
 #pragma unroll
-    for (int i = 0; i < NG; i++) {
-      const int64_t gi = min((kb * kRowsBlockK + 32 * GS * i) >> p.gshift, p.G - 1);
-      const uint32_t z = p.Z ? p.Z[gi * p.ldz + scol] : 8u;
-      sz[i] = p.S[gi * p.lds + scol] | z << 16;
+      for (int i = 0; i < NG; i++) {
+        const int64_t gi = min((k0 + 32 * GS * i) >> p.gshift, p.G - 1);
+        s16[i] = (p.S + gi * p.lds)[scol];
+        z8[i] = (p.Z + gi * p.ldz)[scol];
+      }
     }
 #pragma unroll
-    for (int i = 0; i < LA; i++) a[i] = *(const u32x4 *)(abase + (min((uint32_t)(4 * i + g) * lda, amax) + oa));
+    for (int i = at * LA / 4; i < (at + 1) * LA / 4; i++)
+      a[i] = rows_load(rsa, PART && k0 + 8 * c >= K ? aoff[i] - 16 * c : aoff[i] + (PART ? 2 * k0 : 0), PART ? 0 : 2 * k0);
+    // Loads stay where they are, a quarter before each k step: all of them at
+    // once would hold the wave at the address queue, and left to itself the
+    // compiler moves them behind the products.
+    __builtin_amdgcn_sched_barrier(0x386);   // VALU, SALU and LDS instructions may cross
   };
 
   v4f32 acc[RB][NT];
@@ -354,11 +407,10 @@ __global__ __launch_bounds__((64 * RowsW4<AR, NT>::MAX_WAVES)) void lds_gemm_w4_
     for (int t = 0; t < NT; t++) acc[i][t] = v4f32{0.f, 0.f, 0.f, 0.f};
 
   const v8i16 ones = __builtin_bit_cast(v8i16, u32x4{W4<IN>::ONES, W4<IN>::ONES, W4<IN>::ONES, W4<IN>::ONES});
-  const int blocks = (K + kRowsBlockK - 1) / kRowsBlockK;
-  // One block; LAST: this wave's last one, which may be cut short by K.
-  auto block = [&](int kb, auto last) {
-    constexpr bool LAST = decltype(last)::value;
-    const int left = LAST ? K - kb * kRowsBlockK : kRowsBlockK;   // k of this block that exist
+  const uint32_t mask = w4_constant(W4<IN>::MASK), base = w4_constant(W4<IN>::BASE);
+  // The products of the loaded block, of which the first `left` k exist; next(j)
+  // issues quarter j of the next block's loads.
+  auto block = [&](int left, auto next) {
     wave_lds_order();
 #pragma unroll
     for (int t = 0; t < NT; t++)
@@ -366,18 +418,9 @@ __global__ __launch_bounds__((64 * RowsW4<AR, NT>::MAX_WAVES)) void lds_gemm_w4_
 #pragma unroll
     for (int i = 0; i < LA; i++) *(u32x4 *)(sa + kc_chunk_offset(4 * i + g, c, AROW)) = w4_pairs(a[i]);
     wave_lds_order();
-    float s[NG][NT], z[NG][NT];
+    uint32_t sz[NG];                     // scale | zero point << 16
 #pragma unroll
-    for (int i = 0; i < NG; i++) {
-      uint32_t v[NT];
-      spread_rows<NT>(v, sz[i]);
-#pragma unroll
-      for (int t = 0; t < NT; t++) {
-        s[i][t] = to_f32<IN>((uint16_t)v[t]);
-        z[i][t] = 16.f + (float)(v[t] >> 16);
-      }
-    }
-    if constexpr (!LAST) load(kb + waves);
+    for (int i = 0; i < NG; i++) sz[i] = s16[i] | ((z8[i] & p.zmask) + p.zadd) << 16;
     u32x4 w[NT];
 #pragma unroll
     for (int t = 0; t < NT; t++)
@@ -393,6 +436,7 @@ __global__ __launch_bounds__((64 * RowsW4<AR, NT>::MAX_WAVES)) void lds_gemm_w4_
       }
 #pragma unroll
       for (int j = gi * GS; j < (gi + 1) * GS; j++) {
+        next(j);
         if (32 * j < left) {
           v8i16 fa[RB];
 #pragma unroll
@@ -403,27 +447,44 @@ __global__ __launch_bounds__((64 * RowsW4<AR, NT>::MAX_WAVES)) void lds_gemm_w4_
           }
 #pragma unroll
           for (int t = 0; t < NT; t++) {
-            const v8i16 fb = w4_unpack<IN>(w[t][j]);
+            const v8i16 fb = w4_unpack<IN>(w[t][j], mask, base);
 #pragma unroll
             for (int i = 0; i < RB; i++) part[i][t] = mfma_16x16x32<IN>(fa[i], fb, part[i][t]);
           }
         }
       }
       if (32 * gi * GS < left) {
+        uint32_t v[NT];
+        spread_rows<NT>(v, sz[gi]);
 #pragma unroll
-        for (int t = 0; t < NT; t++)
+        for (int t = 0; t < NT; t++) {
+          const float s = to_f32<IN>((uint16_t)v[t]), z = 16.f + (float)(v[t] >> 16);
 #pragma unroll
           for (int i = 0; i < RB; i++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) acc[i][t][r] += s[gi][t] * (part[i][t][r] - z[gi][t] * sum[i][r]);
+            for (int r = 0; r < 4; r++) acc[i][t][r] += s * (part[i][t][r] - z * sum[i][r]);
+        }
       }
     }
   };
-  if (wave < blocks) {
-    int kb = wave;
-    load(kb);
-    for (; kb + waves < blocks; kb += waves) block(kb, std::false_type{});
-    block(kb, std::true_type{});
+  // Whole blocks go round the waves; the last wave takes the cut one first.
+  const int full = K / kRowsBlockK, left = K % kRowsBlockK;
+  int kb = wave;
+  const std::false_type whole{};
+  const auto load_all = [&](int at, auto part) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) load(at, j, part);
+  };
+  if (left != 0 && wave == waves - 1) {
+    load_all(full, std::true_type{});
+    block(left, [](int) {});
+  }
+  if (kb < full) {
+    const int start = rows_start(full);
+    auto at = [&](int b) { return b + start < full ? b + start : b + start - full; };
+    load_all(at(kb), whole);
+    for (; kb + waves < full; kb += waves) block(kRowsBlockK, [&](int j) { load(at(kb + waves), j, whole); });
+    block(kRowsBlockK, [](int) {});
   }
 
   __syncthreads();                       // the partial sums take the slices' place

@@ -200,6 +200,10 @@ __device__ __forceinline__ void finish_chunk(const NormArgs &p, int64_t m, const
   }
 }
 
+// The workgroup's number in a grid of two dimensions: one of them holds fewer
+// than 2^32 threads.
+__device__ __forceinline__ int64_t workgroup() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // One row to a workgroup, V chunks to a thread (8 <= N <= 8 V threads), or,
 // with ROWS > 1, one row to each of ROWS waves (N <= 512).  Every element is
 // read before the reduction and written after it, so an output may stand in
@@ -208,8 +212,8 @@ template <int IN, bool Q8, int V, int ROWS>
 __global__ __launch_bounds__(ROWS > 1 ? 64 * ROWS : 1024) void rmsnorm_kernel(const NormArgs p) {
   const int threads = ROWS > 1 ? 64 : blockDim.x;
   const int t = ROWS > 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t m = ROWS > 1 ? (int64_t)blockIdx.x * ROWS + (threadIdx.x >> 6) : blockIdx.x;
-  if (m >= p.M) return;                  // whole waves, of rows that meet no barrier
+  const int64_t m = ROWS > 1 ? workgroup() * ROWS + (threadIdx.x >> 6) : workgroup();
+  if (m >= p.M) return;                  // whole waves of rows that meet no barrier, or whole workgroups
   float h[V][kChunk], w[V][kChunk];
   float sum = 0.f;
   uint32_t top = 0;
@@ -231,7 +235,8 @@ __global__ __launch_bounds__(ROWS > 1 ? 64 * ROWS : 1024) void rmsnorm_kernel(co
 // may stand in an input's place.
 template <int IN, bool Q8>
 __global__ __launch_bounds__(1024) void rmsnorm_any_kernel(const NormArgs p) {
-  const int64_t m = blockIdx.x;
+  const int64_t m = workgroup();
+  if (m >= p.M) return;
   const int chunks = p.N / kChunk, tail = kChunk * chunks + threadIdx.x;
   const uint16_t *x = p.X + m * p.ldx, *r = p.R + m * p.ldr;
   float sum = 0.f, ht = 0.f, wt = 0.f;
@@ -268,7 +273,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_any_kernel(const NormArgs p) {
 static hipError_t launch_norm(const void *kernel, const NormArgs &p, int64_t blocks, int threads, hipStream_t s) {
   NormArgs a = p;
   void *params[] = {&a};
-  return hipLaunchKernel(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), params, 0, s);
+  const int64_t x = blocks < (1 << 21) ? blocks : 1 << 21;
+  return hipLaunchKernel(kernel, dim3((unsigned)x, (unsigned)ceil_div(blocks, x)), dim3((unsigned)threads), params, 0, s);
 }
 
 template <int IN, bool Q8>

@@ -24,11 +24,12 @@ static hipError_t launch_scaled(const Args &a, int la, int lb, int dtype, hipStr
   }
 }
 
+// Waves of a workgroup: as many as K has blocks for, up to eight.
 template <int AR, int NT, int OUT>
 static hipError_t launch_rows(const Args &a, hipStream_t stream, RowColScale sc) {
   using T = RowsE4M3<AR, NT>;
   int waves = 1;
-  while (2 * waves <= T::MAX_WAVES && 2 * waves * kRowsBlockK <= a.K) waves *= 2;
+  while (2 * waves <= kRowsMaxWaves && 2 * waves * kRowsBlockK <= a.K) waves *= 2;
   const char *A = (const char *)a.A, *B = (const char *)a.B;
   void *C = a.C;
   int M = a.M, N = a.N, K = a.K;
@@ -51,22 +52,34 @@ static hipError_t launch_rows_out(const Args &a, int dtype, hipStream_t s, const
   }
 }
 
-// Column blocks by N: the widest tile that still makes a workgroup for every
-// CU; then as many waves as K has blocks for.
+// Column blocks by M and N: two if that still makes a workgroup for every CU;
+// one where at most 8 rows make the activations' share small (1 x 16384 x 8192:
+// 23.6 us with one, 25.7 with two).
 template <int AR>
 static hipError_t dispatch_rows(const Args &a, int dtype, hipStream_t s, const RowColScale &sc) {
-  const int nt = ceil_div(a.N, 64) >= 256 ? 4 : ceil_div(a.N, 32) >= 256 ? 2 : 1;
-  if (nt == 4) return launch_rows_out<AR, 4>(a, dtype, s, sc);
-  if (nt == 2) return launch_rows_out<AR, 2>(a, dtype, s, sc);
+  if (AR > 8 && ceil_div(a.M, AR < 16 ? 16 : AR) * ceil_div(a.N, 32) >= 256)
+    return launch_rows_out<AR, 2>(a, dtype, s, sc);
   return launch_rows_out<AR, 1>(a, dtype, s, sc);
 }
 
-// The shape classes of gemm_run's E4M3 products; at most 32 rows with both
-// operands K-contiguous take the few-rows kernel.
+// With both operands K-contiguous the few-rows kernel takes M <= 48, and up to
+// 192 rows while 64 x 64 tiles would fill no more than half of the CUs, each
+// walking all of K.  bf16 output, the few-rows kernel against the 64 x 64 tiles:
+// 33 x 16384 x 8192 31 and 35 us, 64 x 8192 x 8192 17 and 30, 128 x 4096 x 4096 11
+// and 17, 192 x 1152 x 896 5.0 and 5.4; but 64 x 16384 x 8192 43 and 36,
+// 128 x 8192 x 8192 36 and 32, 256 x 4096 x 4096 20 and 18.
+static bool few_rows(const Args &a, int la, int lb) {
+  return la == KC && lb == KC &&
+         (a.M <= 48 || (a.M <= 192 && ceil_div(a.M, 64) * ceil_div(a.N, 64) <= 128));
+}
+
+// Otherwise the shape classes of gemm_run's E4M3 products.
 static hipError_t dispatch_scaled(const Args &a, int la, int lb, int dtype, hipStream_t s, const RowColScale &sc) {
-  if (a.M <= 32 && la == KC && lb == KC) {
+  if (few_rows(a, la, lb)) {
     if (a.M <= 8) return dispatch_rows<8>(a, dtype, s, sc);
-    return a.M <= 16 ? dispatch_rows<16>(a, dtype, s, sc) : dispatch_rows<32>(a, dtype, s, sc);
+    if (a.M <= 16) return dispatch_rows<16>(a, dtype, s, sc);
+    if (a.M <= 32) return dispatch_rows<32>(a, dtype, s, sc);
+    return a.M <= 48 ? dispatch_rows<48>(a, dtype, s, sc) : dispatch_rows<64>(a, dtype, s, sc);
   }
   if (a.M <= 32) return launch_scaled<SkinnyStream8, SKINNY, IN_E4M3_AS_BF16>(a, la, lb, dtype, s, sc);
   if (ceil_div(a.M, 256) * ceil_div(a.N, 256) >= 256)

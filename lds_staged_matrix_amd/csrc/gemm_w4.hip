@@ -20,22 +20,25 @@ static hipError_t launch_w4(const W4Args &p, int waves, hipStream_t stream) {
                          params, (size_t)waves * (T::SLICE > 1024 * T::RB * NT ? T::SLICE : 1024 * T::RB * NT), stream);
 }
 
+// Waves of a workgroup: as many as K has blocks for, up to eight.  (Sixteen
+// halve the registers, and took 16.2 us for 1 x 16384 x 8192 where eight took
+// 14.1.)
 template <int IN, int AR, int NT>
 static hipError_t launch_w4_group(const W4Args &p, hipStream_t s) {
   int waves = 1;
-  while (2 * waves <= RowsW4<AR, NT>::MAX_WAVES && 2 * waves * kRowsBlockK <= p.K) waves *= 2;
+  while (2 * waves <= kRowsMaxWaves && 2 * waves * kRowsBlockK <= p.K) waves *= 2;
   if (p.gshift == 5) return launch_w4<IN, AR, NT, 1>(p, waves, s);
   if (p.gshift == 6) return launch_w4<IN, AR, NT, 2>(p, waves, s);
   return launch_w4<IN, AR, NT, 4>(p, waves, s);
 }
 
-// Row blocks by M, column blocks by N: the widest tile that still makes a
-// workgroup for every CU; then as many waves as K has blocks for.
+// Column blocks by M and N: two if that still makes a workgroup for every CU
+// (measured with one and two: 16 x 8192 x 8192 12.0 and 10.6 us, 16 x 4096 x
+// 4096 6.0 and 6.8).
 template <int IN, int AR>
 static hipError_t launch_w4_rows(const W4Args &p, hipStream_t s) {
   const int64_t rows = ceil_div(p.M, AR < 16 ? 16 : AR);
-  const int nt = rows * ceil_div(p.N, 64) >= 256 ? 4 : rows * ceil_div(p.N, 32) >= 256 ? 2 : 1;
-  if (nt == 4) return launch_w4_group<IN, AR, 4>(p, s);
+  const int nt = rows * ceil_div(p.N, 32) >= 256 ? 2 : 1;
   if (nt == 2) return launch_w4_group<IN, AR, 2>(p, s);
   return launch_w4_group<IN, AR, 1>(p, s);
 }
@@ -45,7 +48,7 @@ static hipError_t dispatch_w4(const W4Args &p, hipStream_t s) {
   if (p.M <= 4) return launch_w4_rows<IN, 4>(p, s);
   if (p.M <= 16) return launch_w4_rows<IN, 16>(p, s);
   if (p.M <= 32) return launch_w4_rows<IN, 32>(p, s);
-  if (p.M <= 48 && p.M > 32) return launch_w4_rows<IN, 48>(p, s);
+  if (p.M <= 48) return launch_w4_rows<IN, 48>(p, s);
   return launch_w4_rows<IN, 64>(p, s);
 }
 
@@ -88,9 +91,10 @@ extern "C" int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const 
 
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess || dev != h->device) return GEMM_ERR_DEVICE;
-  const W4Args p{(const uint16_t *)A, (const uint8_t *)B, (const uint16_t *)S, (const uint8_t *)Z, C,
+  // Without zero points the kernel reads S's first row in their place and counts 8.
+  const W4Args p{(const uint16_t *)A, (const uint8_t *)B, (const uint16_t *)S, (const uint8_t *)(Z ? Z : S), C,
                  (int)M, (int)N, (int)K, (int)G, __builtin_ctzll((unsigned long long)group),
-                 lda, ldb / 2, lds, ldz, ldc, 1, out_f32 ? 1 : 0};
+                 lda, ldb / 2, lds, Z ? ldz : 0, ldc, 1, out_f32 ? 1 : 0, Z ? 255u : 0u, Z ? 0u : 8u};
   const bool bf16 = dtype == GEMM_BF16_F32 || dtype == GEMM_BF16_BF16;
   const hipError_t e = bf16 ? dispatch_w4<IN_BF16>(p, stream) : dispatch_w4<IN_F16>(p, stream);
   return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;

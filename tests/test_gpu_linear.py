@@ -133,6 +133,20 @@ def test_norm_many_rows(M):
     check_norm(M, 384, "bf16", "e4m3", run_norm(M, 384, "bf16", "e4m3", True, True))
 
 
+def test_norm_more_rows_than_one_grid_dimension_holds():
+    M = (1 << 26) + 3                    # of 64 threads each
+    X = torch.full((M, 1), 2.0, dtype=torch.bfloat16, device="cuda")
+    X[-1] = 0
+    W = torch.ones(1, dtype=torch.bfloat16, device="cuda")
+    Y, S = torch.zeros(M, 1, dtype=FP8, device="cuda"), torch.zeros(M, device="cuda")
+    print("CASE norm rows", M, flush=True)
+    ok(lsm.gemm_rmsnorm_run(H.handle(), X, None, W, None, Y, S, M, 1, 1, 0, 0, 1, 0.0, lsm.GEMM_NORM_BF16_E4M3,
+                            torch.cuda.current_stream()), "gemm_rmsnorm_run")
+    # 448 is the byte 0x7E; a row of zeros with eps 0 has no root
+    assert int((Y.view(torch.uint8)[:-1] != 0x7E).sum()) == 0 and bool(S[:-1].eq(1 / 448).all())
+    assert bool(S[-1].isnan()) and int(Y.view(torch.uint8)[-1]) & 0x7F == 0x7F
+
+
 def test_norm_h_without_residual_and_residual_without_h():
     check_norm(4, 640, "bf16", "bf16", run_norm(4, 640, "bf16", "bf16", False, True))
     check_norm(4, 640, "bf16", "e4m3", run_norm(4, 640, "bf16", "e4m3", True, False))
