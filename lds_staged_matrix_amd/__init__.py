@@ -1,8 +1,9 @@
 """Python binding of the LDS-staged GEMM C ABI (include/lds_gemm.h).
 
 Argument marshalling only: every step of C <- A*B runs in the HIP library
-liblds_gemm.so built in this directory.  There is no fallback: if the
-library is missing, every entry point raises.
+liblds_gemm.so built in this directory; the calls that enqueue work go through
+_binding.so (csrc/binding.c), the others through ctypes.  There is no fallback:
+if either is missing, the entry points raise.
 
 Names mirror the C ABI: gemm_create, gemm_run, gemm_destroy, gemm_status_str,
 and the operators of a quantised linear layer: gemm_rmsnorm_run (norm with the
@@ -15,7 +16,6 @@ attribute (torch streams) or None for the null stream.
 """
 import ctypes
 import os
-import struct
 
 __all__ = [
     "GEMM_K_CONTIG", "GEMM_MN_CONTIG",
@@ -24,8 +24,8 @@ __all__ = [
     "GEMM_NORM_BF16_BF16", "GEMM_NORM_BF16_E4M3", "GEMM_NORM_F16_F16", "GEMM_NORM_F16_E4M3",
     "GEMM_OK", "GEMM_ERR_INVALID_ARG", "GEMM_ERR_UNSUPPORTED", "GEMM_ERR_DEVICE",
     "GEMM_ERR_LAUNCH", "GemmError", "library_path", "load_library", "gemm_create",
-    "gemm_run", "gemm_scaled_run", "gemm_w4_run", "gemm_rmsnorm_run", "gemm_destroy", "gemm_status_str", "EXPORTED_SYMBOLS", "Library",
-    "ablation_library",
+    "gemm_run", "gemm_scaled_run", "gemm_w4_run", "gemm_rmsnorm_run", "gemm_destroy",
+    "gemm_status_str", "EXPORTED_SYMBOLS", "Library", "ablation_library",
 ]
 
 GEMM_K_CONTIG, GEMM_MN_CONTIG = 0, 1
@@ -39,6 +39,7 @@ EXPORTED_SYMBOLS = ("gemm_create", "gemm_run", "gemm_scaled_run", "gemm_w4_run",
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "liblds_gemm.so"
 _lib = None
+_native = None
 
 
 class GemmError(RuntimeError):
@@ -72,32 +73,30 @@ def load_library():
     """Load liblds_gemm.so (raises if it has not been built)."""
     global _lib
     if _lib is None:
-        lib = _open(library_path())
-        vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
-        lib.gemm_scaled_run.argtypes = [vp] * 6 + [i64] * 6 + [i32] * 5 + [vp]
-        lib.gemm_w4_run.argtypes = [vp] * 6 + [i64] * 9 + [i32, vp]
-        lib.gemm_rmsnorm_run.argtypes = [vp] * 7 + [i64] * 6 + [f32, i32, vp]
-        for f in (lib.gemm_scaled_run, lib.gemm_w4_run, lib.gemm_rmsnorm_run):
-            f.restype = i32
-        _lib = lib
+        _lib = _open(library_path())
     return _lib
+
+
+def _bind():
+    """The module _binding (csrc/binding.c) on load_library()'s entry points."""
+    global _native
+    lib = load_library()
+    if not os.path.exists(os.path.join(_HERE, "_binding.so")):
+        raise RuntimeError(f"_binding.so is missing from {_HERE}: build it with lds_staged_matrix_amd/build.py "
+                           "(or __graft_entry__.build()); there is no fallback path")
+    from . import _binding
+    _binding.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                    for name in ("gemm_run", "gemm_scaled_run", "gemm_w4_run", "gemm_rmsnorm_run")))
+    _native = _binding
+    return _native
 
 
 def _ptr(x):
     if x is None:
         return None
-    try:
+    if hasattr(x, "data_ptr"):
         return x.data_ptr()
-    except AttributeError:
-        return int(x)
-
-
-def _ptrs(*xs):
-    """_ptr of each, in one go for what torch programs pass."""
-    try:
-        return [None if x is None else x.data_ptr() for x in xs]
-    except AttributeError:
-        return [_ptr(x) for x in xs]
+    return int(x)
 
 
 def _int(x, bits, name):
@@ -109,36 +108,19 @@ def _int(x, bits, name):
     return v
 
 
-class _Ints:
-    """The integer parameters of an entry point, in order: `wide` int64_t, then
-    `narrow` int32_t ones.  A small call's time is mostly its host part, so all
-    are converted and checked in one go; one that does not fit raises."""
-
-    def __init__(self, wide, narrow):
-        self.names = [(n, 64) for n in wide.split()] + [(n, 32) for n in narrow.split()]
-        fmt = struct.Struct("=%dq%di" % (len(wide.split()), len(narrow.split())))
-        self.pack, self.unpack = fmt.pack, fmt.unpack
-
-    def __call__(self, *values):
-        try:
-            return self.unpack(self.pack(*values))
-        except struct.error:        # too large, or not an integer type
-            return [_int(v, bits, name) for v, (name, bits) in zip(values, self.names)]
-
-
-_RUN = _Ints("M N K lda ldb ldc", "layoutA layoutB dtype")
-_SCALED = _Ints("M N K lda ldb ldc", "incA incB layoutA layoutB dtype")
-_W4 = _Ints("M N K group lda ldb lds ldz ldc", "dtype")
-_NORM = _Ints("M N ldx ldr ldh ldy", "dtype")
+def _sizes(M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype):
+    return ([_int(v, 64, n) for v, n in zip((M, N, K, lda, ldb, ldc),
+                                             ("M", "N", "K", "lda", "ldb", "ldc"))] +
+            [_int(v, 32, n) for v, n in zip((layoutA, layoutB, dtype),
+                                             ("layoutA", "layoutB", "dtype"))])
 
 
 def _stream(s):
     if s is None:
         return None
-    try:
+    if hasattr(s, "cuda_stream"):
         return s.cuda_stream
-    except AttributeError:
-        return int(s)
+    return int(s)
 
 
 def gemm_create():
@@ -152,30 +134,24 @@ def gemm_create():
 
 def gemm_run(h, A, B, C, M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype, stream=None) -> int:
     """Enqueue C <- A*B; returns the gemm_status code (0 on success)."""
-    return load_library().gemm_run(h, _ptr(A), _ptr(B), _ptr(C),
-                                   *_RUN(M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype),
-                                   _stream(stream))
+    return (_native or _bind()).run(h, A, B, C, M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype, stream)
 
 
 def gemm_scaled_run(h, A, B, C, SA, SB, M, N, K, lda, ldb, ldc, incA, incB, layoutA, layoutB, dtype,
                     stream=None) -> int:
     """Enqueue C <- diag(SA) A B diag(SB) for E4M3 operands; returns the gemm_status code."""
-    return load_library().gemm_scaled_run(
-        h, *_ptrs(A, B, C, SA, SB),
-        *_SCALED(M, N, K, lda, ldb, ldc, incA, incB, layoutA, layoutB, dtype), _stream(stream))
+    return (_native or _bind()).scaled(h, A, B, C, SA, SB, M, N, K, lda, ldb, ldc, incA, incB, layoutA, layoutB,
+                                       dtype, stream)
 
 
 def gemm_w4_run(h, A, B, S, Z, C, M, N, K, group, lda, ldb, lds, ldz, ldc, dtype, stream=None) -> int:
     """Enqueue the product of 16-bit rows with 4-bit weights; returns the gemm_status code."""
-    return load_library().gemm_w4_run(h, *_ptrs(A, B, S, Z, C),
-                                      *_W4(M, N, K, group, lda, ldb, lds, ldz, ldc, dtype), _stream(stream))
+    return (_native or _bind()).w4(h, A, B, S, Z, C, M, N, K, group, lda, ldb, lds, ldz, ldc, dtype, stream)
 
 
 def gemm_rmsnorm_run(h, X, R, W, H, Y, S, M, N, ldx, ldr, ldh, ldy, eps, dtype, stream=None) -> int:
     """Enqueue the RMS norm of X (+ R); returns the gemm_status code."""
-    M, N, ldx, ldr, ldh, ldy, dtype = _NORM(M, N, ldx, ldr, ldh, ldy, dtype)
-    return load_library().gemm_rmsnorm_run(h, *_ptrs(X, R, W, H, Y, S), M, N, ldx, ldr, ldh, ldy, eps, dtype,
-                                           _stream(stream))
+    return (_native or _bind()).rmsnorm(h, X, R, W, H, Y, S, M, N, ldx, ldr, ldh, ldy, eps, dtype, stream)
 
 
 def gemm_destroy(h) -> int:
@@ -205,7 +181,7 @@ class Library:
     def gemm_run(self, h, A, B, C, M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype,
                  stream=None) -> int:
         return self._lib.gemm_run(h, _ptr(A), _ptr(B), _ptr(C),
-                                  *_RUN(M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype),
+                                  *_sizes(M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype),
                                   _stream(stream))
 
     def gemm_destroy(self, h) -> int:

@@ -1,6 +1,7 @@
 """Build the HIP library liblds_gemm.so in-tree with hipcc for gfx950.
 
 Also builds, from the same sources:
+  * _binding.so -- the Python side of its enqueueing entry points (host C);
   * ablation/liblds_gemm_<name>.so -- the A/B builds that each change one
     design choice (see VARIANTS), used by the benchmark and the counter runs
     that measure what each choice buys;
@@ -12,12 +13,14 @@ Also builds, from the same sources:
 """
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblds_gemm.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ABLATION_DIR = os.path.join(PKG, "ablation")
 SOURCES = ["gemm_api.hip", "gemm_scaled.hip", "gemm_w4.hip", "gemm_norm.hip"]
 VARIANT_SOURCES = ["gemm_api.hip"]     # the A/B builds change gemm_run's kernels
@@ -66,7 +69,7 @@ def _run(cmd, out, verbose):
     errs = "\n".join(l for l in res.stderr.splitlines()
                      if "packed-fp32-ops" not in l)   # host pass does not know the feature
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{errs}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}):\n{errs}")
     if verbose and errs.strip():
         print(errs)
     os.replace(out + ".tmp", out)
@@ -83,6 +86,7 @@ def build(verbose: bool = False, extra_flags=(), variant: str = None) -> str:
         return _run(cmd, out, verbose)
     with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
         objs = list(pool.map(lambda s: build_object(s, verbose, extra_flags), SOURCES))
+    build_binding(verbose)
     return _run([HIPCC, *FLAGS, "-shared", *objs, "-o", LIB + ".tmp"], LIB, verbose)
 
 
@@ -92,6 +96,14 @@ def build_object(source: str, verbose: bool = False, extra_flags=()) -> str:
     out = os.path.join(OBJ_DIR, os.path.splitext(source)[0] + ".o")
     cmd = [HIPCC, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, source), "-o", out + ".tmp"]
     return _run(cmd, out, verbose)
+
+
+def build_binding(verbose: bool = False) -> str:
+    """The Python side of the entry points (host C, CPython C API)."""
+    cmd = ["gcc", "-O2", "-std=gnu11", "-Wall", "-shared", "-fPIC", "-D__HIP_PLATFORM_AMD__",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), "-I", "/opt/rocm/include",
+           os.path.join(CSRC, "binding.c"), "-o", BINDING + ".tmp"]
+    return _run(cmd, BINDING, verbose)
 
 
 def build_hw_probe(verbose: bool = False) -> str:

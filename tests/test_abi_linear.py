@@ -142,6 +142,38 @@ def test_integers_that_the_abi_cannot_hold(fn, base, name, value):
         call(fn, base, {name: value})
 
 
+class Pointer:
+    def __init__(self, value):
+        self.value = value
+
+    def data_ptr(self):
+        if isinstance(self.value, Exception):
+            raise self.value
+        return self.value
+
+
+def test_what_the_binding_takes():
+    """numpy and float sizes, pointer objects, stream objects, integer handles; errors pass through."""
+    np = pytest.importorskip("numpy")
+    run = lsm.gemm_w4_run
+    assert call(run, W4, dict(M=np.int64(4), N=np.int32(48), K=96.0)) == VALID
+    assert call(run, W4, {k: Pointer(v) for k, v in W4.items() if k in "ABSZC"}) == VALID
+    assert call(run, W4, dict(A=Pointer(addr(0) + 8))) == UNSUPPORTED
+    assert call(run, W4, dict(A=Pointer(0))) == INVALID
+    assert call(run, W4, dict(h=ctypes.addressof(_FAKE_DEVICE))) == VALID
+    assert call(run, W4, dict(stream=type("Stream", (), {"cuda_stream": 0})())) == VALID
+    assert call(run, W4, dict(stream=0)) == VALID
+    with pytest.raises(ValueError, match="gone"):
+        call(run, W4, dict(A=Pointer(ValueError("gone"))))
+    with pytest.raises((TypeError, ValueError)):
+        call(run, W4, dict(M="many"))
+    with pytest.raises(TypeError):
+        call(lsm.gemm_rmsnorm_run, NORM, dict(eps="small"))
+    from lds_staged_matrix_amd import _binding
+    with pytest.raises(TypeError, match="gemm_run takes 14 arguments, got 1"):
+        _binding.run(None)
+
+
 def test_the_plain_product_refuses_the_scaled_product_s_type():
     assert lsm.gemm_run(FAKE, addr(0), addr(1), addr(2), 16, 16, 16, 16, 16, 16, 0, 0,
                         lsm.GEMM_E4M3_F16) == INVALID
