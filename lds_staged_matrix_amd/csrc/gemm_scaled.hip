@@ -1,12 +1,14 @@
 // gemm_scaled.hip -- gemm_scaled_run: the E4M3 product whose rows and columns
 // carry fp32 scales.  The kernels are gemm_run's, with the scales applied to
-// the fp32 sums before they are rounded (scale_acc in gemm_common.h), and the
-// few-rows kernel of gemm_kernel_rows.h.
+// the fp32 sums before they are rounded (scale_acc in gemm_common.h), the
+// few-rows kernel of gemm_kernel_rows.h and the split-K tile of
+// gemm_kernel_splitk.h.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
 
 #include "gemm_kernel_rows.h"
+#include "gemm_kernel_splitk.h"
 #include "gemm_launch.h"
 
 namespace lsm {
@@ -22,6 +24,59 @@ static hipError_t launch_scaled(const Args &a, int la, int lb, int dtype, hipStr
     case GEMM_E4M3_BF16: return launch_layout<T, KIND, IN16, OUT_BF16, RowColScale>(a, la, lb, s, sc);
     default: return launch_layout<T, KIND, IN16, OUT_F16, RowColScale>(a, la, lb, s, sc);
   }
+}
+
+template <int LA, int LB, int IN, int OUT, int KS, int NS>
+static hipError_t launch_splitk(const Args &a, hipStream_t stream, RowColScale sc) {
+  using T = DmaSmall8;
+  int tiles_m = (int)ceil_div(a.M, T::BM), tiles_n = (int)ceil_div(a.N, T::BN);
+  const uint16_t *A = a.A, *B = a.B;
+  void *C = a.C;
+  int M = a.M, N = a.N, K = a.K;
+  int64_t lda = a.lda, ldb = a.ldb, ldc = a.ldc;
+  uint32_t ab = a.a_bytes, bb = a.b_bytes;
+  constexpr int64_t esz = OUT == OUT_F32 ? 4 : 2;
+  int c_vec = ((uintptr_t)C % 16 == 0) && ((ldc * esz) % 16 == 0);
+  void *params[] = {&A, &B, &C, &M, &N, &K, &lda, &ldb, &ldc, &tiles_m, &tiles_n, &ab, &bb, &c_vec, &sc};
+  return hipLaunchKernel((const void *)lds_gemm_splitk_kernel<T, LA, LB, IN, OUT, KS, NS>,
+                         dim3((unsigned)(tiles_m * tiles_n)), dim3(KS * T::NT), params, 0, stream);
+}
+
+template <int KS, int NS, int IN, int OUT>
+static hipError_t launch_splitk_layout(const Args &a, int la, int lb, hipStream_t s, const RowColScale &sc) {
+  if (la == KC && lb == KC) return launch_splitk<KC, KC, IN, OUT, KS, NS>(a, s, sc);
+  if (la == KC && lb == MNC) return launch_splitk<KC, MNC, IN, OUT, KS, NS>(a, s, sc);
+  if (la == MNC && lb == KC) return launch_splitk<MNC, KC, IN, OUT, KS, NS>(a, s, sc);
+  return launch_splitk<MNC, MNC, IN, OUT, KS, NS>(a, s, sc);
+}
+
+// Products of at most 256 tiles of 64 x 64 (one for a CU) share each tile's K
+// out over groups of waves once it is 1024 long: two groups with four LDS
+// stages, or four with two for fp32 output, whose conversions want the waves.
+// Up to 1024 tiles and from K = 4096 on, two groups with two stages, so that
+// two workgroups fit a CU.  Kernel times against the kernels without the split:
+//   bf16 output  256 x 4096 x 4096 12.2 and 18.2 us, 256 x 2048 x 8192 16.9 and
+//   32.1, 128 x 8192 x 8192 18.1 and 29.9, 512 x 8192 x 8192 55 and 67, 1024 x
+//   4096 x 4096 31 and 35; but 1500 x 1152 x 896 8.3 and 6.8, 2048 x 4096 x 4096
+//   65 and 47.
+//   fp32 output  256 x 4096 x 4096 14.1 and 18.7 us, 256 x 2048 x 8192 20.2 and
+//   32.4, 512 x 8192 x 8192 77 and 89.
+// Returns false where the split does not pay.
+static bool dispatch_splitk(const Args &a, int la, int lb, int dtype, hipStream_t s, const RowColScale &sc,
+                            hipError_t &e) {
+  const int64_t tiles = ceil_div(a.M, 64) * ceil_div(a.N, 64);
+  const bool f32 = dtype == GEMM_E4M3_F32, bf16 = dtype == GEMM_E4M3_BF16;
+  if (tiles <= 256 && a.K >= 1024)
+    e = f32    ? launch_splitk_layout<4, 2, IN_E4M3_AS_BF16, OUT_F32>(a, la, lb, s, sc)
+        : bf16 ? launch_splitk_layout<2, 4, IN_E4M3, OUT_BF16>(a, la, lb, s, sc)
+               : launch_splitk_layout<2, 4, IN_E4M3, OUT_F16>(a, la, lb, s, sc);
+  else if (tiles > 256 && tiles <= 1024 && a.K >= 4096)
+    e = f32    ? launch_splitk_layout<2, 2, IN_E4M3_AS_BF16, OUT_F32>(a, la, lb, s, sc)
+        : bf16 ? launch_splitk_layout<2, 2, IN_E4M3, OUT_BF16>(a, la, lb, s, sc)
+               : launch_splitk_layout<2, 2, IN_E4M3, OUT_F16>(a, la, lb, s, sc);
+  else
+    return false;
+  return true;
 }
 
 // Waves of a workgroup: as many as K has blocks for, up to eight.
@@ -73,7 +128,8 @@ static bool few_rows(const Args &a, int la, int lb) {
          (a.M <= 48 || (a.M <= 192 && ceil_div(a.M, 64) * ceil_div(a.N, 64) <= 128));
 }
 
-// Otherwise the shape classes of gemm_run's E4M3 products.
+// Otherwise the split-K tiles where they pay, and the shape classes of
+// gemm_run's E4M3 products.
 static hipError_t dispatch_scaled(const Args &a, int la, int lb, int dtype, hipStream_t s, const RowColScale &sc) {
   if (few_rows(a, la, lb)) {
     if (a.M <= 8) return dispatch_rows<8>(a, dtype, s, sc);
@@ -82,6 +138,8 @@ static hipError_t dispatch_scaled(const Args &a, int la, int lb, int dtype, hipS
     return a.M <= 48 ? dispatch_rows<48>(a, dtype, s, sc) : dispatch_rows<64>(a, dtype, s, sc);
   }
   if (a.M <= 32) return launch_scaled<SkinnyStream8, SKINNY, IN_E4M3_AS_BF16>(a, la, lb, dtype, s, sc);
+  hipError_t e;
+  if (dispatch_splitk(a, la, lb, dtype, s, sc, e)) return e;
   if (ceil_div(a.M, 256) * ceil_div(a.N, 256) >= 256)
     return launch_scaled<PingPong8, PINGPONG>(a, la, lb, dtype, s, sc);
   if (ceil_div(a.M, 128) * ceil_div(a.N, 128) >= 256)

@@ -238,8 +238,10 @@ def check_scaled(M, N, K, la, lb, out, dist, incs=(1, 1), extra=0):
 LAYOUTS = [(KC, KC), (KC, MNC), (MNC, KC), (MNC, MNC)]
 
 
-@pytest.mark.parametrize("M,N,K", [(4112, 4096, 144), (2064, 2048, 144), (528, 272, 160), (512, 512, 8192),
-                                   (32, 1024, 1040)])
+# ping-pong, 128 x 128, 64 x 64 with two and with four stages, split K with up to
+# and over 256 tiles (each also cut short in all extents), M <= 32
+@pytest.mark.parametrize("M,N,K", [(4112, 4096, 144), (2064, 2048, 144), (528, 272, 160), (1040, 2560, 3984),
+                                   (512, 512, 8192), (208, 1040, 1040), (1040, 1088, 4112), (32, 1024, 1040)])
 @pytest.mark.parametrize("la,lb", LAYOUTS)
 @pytest.mark.parametrize("out", sorted(SCALED))
 def test_scaled_every_kernel(M, N, K, la, lb, out):
@@ -247,11 +249,21 @@ def test_scaled_every_kernel(M, N, K, la, lb, out):
         check_scaled(M, N, K, la, lb, out, dist)
 
 
-@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 31, 32, 33])
+@pytest.mark.parametrize("M", [1, 2, 8, 15, 16, 17, 31, 32, 33, 48, 49, 65, 190])
 @pytest.mark.parametrize("N,K", [(1, 16), (17, 48), (100, 128), (257, 1040), (4099, 144), (8209, 272), (16400, 160)])
 def test_scaled_few_rows(M, N, K):
     for dist in ("int", "real"):
         check_scaled(M, N, K, KC, KC, "f32" if N % 2 else "bf16", dist, extra=N % 3)
+
+
+@pytest.mark.parametrize("M,N", [(201, 333), (1000, 1101)])
+@pytest.mark.parametrize("K", [1024, 1152, 1168, 4096, 4112, 4240])
+@pytest.mark.parametrize("out", ["f16", "f32"])
+def test_scaled_split_k_ragged(M, N, K, out):
+    """Steps that do not divide over the groups, cut tiles, rows of C at odd pitches."""
+    for extra in (0, 3):
+        check_scaled(M, N, K, KC, KC, out, "int", extra=extra)
+    check_scaled(M, N, K, KC, KC, out, "real")
 
 
 @pytest.mark.parametrize("K", [16, 112, 128, 144, 256, 1936, 2048, 4096, 8208])
