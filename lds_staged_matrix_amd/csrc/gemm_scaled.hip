@@ -140,9 +140,15 @@ static hipError_t dispatch_scaled(const Args &a, int la, int lb, int dtype, hipS
   if (a.M <= 32) return launch_scaled<SkinnyStream8, SKINNY, IN_E4M3_AS_BF16>(a, la, lb, dtype, s, sc);
   hipError_t e;
   if (dispatch_splitk(a, la, lb, dtype, s, sc, e)) return e;
-  if (ceil_div(a.M, 256) * ceil_div(a.N, 256) >= 256)
+  // The 256 x 256 tile also wins with fewer workgroups than CUs where it
+  // replaces more than two rounds of 128 x 128 tiles.  bf16 output, ping-pong
+  // against 128 x 128: 1100 x 8192 x 8192 79 and 141 us, 2048 x 5000 x 3200 42 and
+  // 61, 1500 x 6000 x 1024 19.5 and 25.7; at two rounds 2048 x 4096 x 4096 47 and
+  // 46, 1024 x 8192 x 8192 97 and 89 (fp32 output 86 and 79, 164 and 165).
+  const int64_t t128 = ceil_div(a.M, 128) * ceil_div(a.N, 128);
+  if (ceil_div(a.M, 256) * ceil_div(a.N, 256) >= 256 || t128 > 512)
     return launch_scaled<PingPong8, PINGPONG>(a, la, lb, dtype, s, sc);
-  if (ceil_div(a.M, 128) * ceil_div(a.N, 128) >= 256)
+  if (t128 >= 256)
     return launch_scaled<DmaMid8, DMA>(a, la, lb, dtype, s, sc);
   if (small_tile_four_stages(a, 1)) return launch_scaled<DmaSmall8, DMA4>(a, la, lb, dtype, s, sc);
   return launch_scaled<DmaSmall8, DMA>(a, la, lb, dtype, s, sc);

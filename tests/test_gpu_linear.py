@@ -238,9 +238,9 @@ def check_scaled(M, N, K, la, lb, out, dist, incs=(1, 1), extra=0):
 LAYOUTS = [(KC, KC), (KC, MNC), (MNC, KC), (MNC, MNC)]
 
 
-# ping-pong, 128 x 128, 64 x 64 with two and with four stages, split K with up to
+# ping-pong (two of it: 256 tiles and fewer), 128 x 128, 64 x 64 with two and with four stages, split K with up to
 # and over 256 tiles (each also cut short in all extents), M <= 32
-@pytest.mark.parametrize("M,N,K", [(4112, 4096, 144), (2064, 2048, 144), (528, 272, 160), (1040, 2560, 3984),
+@pytest.mark.parametrize("M,N,K", [(4112, 4096, 144), (1040, 8208, 144), (2064, 2048, 144), (528, 272, 160), (1040, 2560, 3984),
                                    (512, 512, 8192), (208, 1040, 1040), (1040, 1088, 4112), (32, 1024, 1040)])
 @pytest.mark.parametrize("la,lb", LAYOUTS)
 @pytest.mark.parametrize("out", sorted(SCALED))
