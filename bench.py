@@ -53,16 +53,25 @@ def _code_only(text):
     return "\n".join(" ".join(l.split()) for l in text.splitlines() if l.strip())
 
 
+def _included(name, seen):
+    """`name` of KERNEL_DIR and the files there that it includes, by name."""
+    path = os.path.join(ROOT, KERNEL_DIR, name)
+    if name not in seen and os.path.exists(path):
+        with open(path, encoding="utf-8") as f:
+            seen[name] = _code_only(f.read())
+        for inc in re.findall(r'^# ?include "([^"]+)"', seen[name], re.M):
+            _included(inc, seen)
+    return seen
+
+
 def kernel_source_hash():
-    """Identity of the kernel sources that the committed profiles were taken on."""
+    """Identity of the kernel sources that the committed profiles were taken on:
+    the source of gemm_run and what it includes, and not those of the library's
+    other entry points or the test probes."""
     h = hashlib.sha256()
-    d = os.path.join(ROOT, KERNEL_DIR)
-    for name in sorted(os.listdir(d)):
-        # the GEMM sources; hw_probe.hip holds test probes, not GEMM kernels
-        if name.endswith((".h", ".hip")) and name != "hw_probe.hip":
-            h.update(name.encode())
-            with open(os.path.join(d, name), encoding="utf-8") as f:
-                h.update(_code_only(f.read()).encode())
+    for name, code in sorted(_included("gemm_api.hip", {}).items()):
+        h.update(name.encode())
+        h.update(code.encode())
     return h.hexdigest()[:16]
 
 
