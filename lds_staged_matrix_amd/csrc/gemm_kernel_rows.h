@@ -298,17 +298,28 @@ struct W4Args {
   uint32_t zmask, zadd;               // zero point = (byte & zmask) + zadd
 };
 
-// One entry, summed term by term in the order of k.
+// One entry, summed term by term in the order of k; 32 of them, which share a
+// scale, are loaded at once.
 template <int IN>
 __device__ __forceinline__ float w4_entry(const W4Args &p, int m, int n) {
   const uint16_t *a = p.A + (int64_t)m * p.lda;
   const uint8_t *b = p.B + (int64_t)n * p.ldb;
   float v = 0.f;
-  for (int k = 0; k < p.K; k++) {
+  for (int k = 0; k < p.K; k += 32) {
     const int64_t gi = k >> p.gshift;
-    const int q = (b[k >> 1] >> (4 * (k & 1))) & 15;
     const int z = (int)((p.Z[gi * p.ldz + n] & p.zmask) + p.zadd);
-    v += to_f32<IN>(a[k]) * ((float)(q - z) * to_f32<IN>(p.S[gi * p.lds + n]));
+    const float s = to_f32<IN>(p.S[gi * p.lds + n]);
+    const u32x4 q = *(const u32x4 *)(b + k / 2);
+    u32x4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) x[j] = *(const u32x4 *)(a + k + 8 * j);
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const uint32_t pair = x[j][i / 2];
+        v += to_f32<IN>((uint16_t)(pair >> (16 * (i & 1)))) * ((float)((int)((q[j] >> (4 * i)) & 15) - z) * s);
+      }
   }
   return v;
 }
