@@ -9,6 +9,23 @@
 
 namespace lsm {
 
+// Rows of a tile, of which so many are loaded; waves of a workgroup: as many as
+// K has blocks for, up to eight (sixteen halve the registers, and took 16.2 us
+// for 1 x 16384 x 8192 where eight took 14.1); column blocks: two if that still
+// makes a workgroup for every CU (measured with one and two: 16 x 8192 x 8192
+// 12.0 and 10.6 us, 16 x 4096 x 4096 6.0 and 6.8).
+static int w4_rows(int64_t M) { return M <= 4 ? 4 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : 64; }
+static int w4_waves(int64_t K) {
+  int waves = 1;
+  while (2 * waves <= kRowsMaxWaves && 2 * waves * kRowsBlockK <= K) waves *= 2;
+  return waves;
+}
+static int64_t w4_row_tiles(int64_t M) {
+  const int rows = w4_rows(M);
+  return ceil_div(M, rows < 16 ? 16 : rows);
+}
+static int w4_column_blocks(int64_t M, int64_t N) { return w4_row_tiles(M) * ceil_div(N, 32) >= 256 ? 2 : 1; }
+
 template <int IN, int AR, int NT, int GS>
 static hipError_t launch_w4(const W4Args &p, int waves, hipStream_t stream) {
   using T = RowsW4<AR, NT>;
@@ -20,36 +37,29 @@ static hipError_t launch_w4(const W4Args &p, int waves, hipStream_t stream) {
                          params, (size_t)waves * (T::SLICE > 1024 * T::RB * NT ? T::SLICE : 1024 * T::RB * NT), stream);
 }
 
-// Waves of a workgroup: as many as K has blocks for, up to eight.  (Sixteen
-// halve the registers, and took 16.2 us for 1 x 16384 x 8192 where eight took
-// 14.1.)
 template <int IN, int AR, int NT>
 static hipError_t launch_w4_group(const W4Args &p, hipStream_t s) {
-  int waves = 1;
-  while (2 * waves <= kRowsMaxWaves && 2 * waves * kRowsBlockK <= p.K) waves *= 2;
+  const int waves = w4_waves(p.K);
   if (p.gshift == 5) return launch_w4<IN, AR, NT, 1>(p, waves, s);
   if (p.gshift == 6) return launch_w4<IN, AR, NT, 2>(p, waves, s);
   return launch_w4<IN, AR, NT, 4>(p, waves, s);
 }
 
-// Column blocks by M and N: two if that still makes a workgroup for every CU
-// (measured with one and two: 16 x 8192 x 8192 12.0 and 10.6 us, 16 x 4096 x
-// 4096 6.0 and 6.8).
 template <int IN, int AR>
-static hipError_t launch_w4_rows(const W4Args &p, hipStream_t s) {
-  const int64_t rows = ceil_div(p.M, AR < 16 ? 16 : AR);
-  const int nt = rows * ceil_div(p.N, 32) >= 256 ? 2 : 1;
-  if (nt == 2) return launch_w4_group<IN, AR, 2>(p, s);
+static hipError_t launch_w4_columns(const W4Args &p, hipStream_t s) {
+  if (w4_column_blocks(p.M, p.N) == 2) return launch_w4_group<IN, AR, 2>(p, s);
   return launch_w4_group<IN, AR, 1>(p, s);
 }
 
 template <int IN>
 static hipError_t dispatch_w4(const W4Args &p, hipStream_t s) {
-  if (p.M <= 4) return launch_w4_rows<IN, 4>(p, s);
-  if (p.M <= 16) return launch_w4_rows<IN, 16>(p, s);
-  if (p.M <= 32) return launch_w4_rows<IN, 32>(p, s);
-  if (p.M <= 48) return launch_w4_rows<IN, 48>(p, s);
-  return launch_w4_rows<IN, 64>(p, s);
+  switch (w4_rows(p.M)) {
+    case 4: return launch_w4_columns<IN, 4>(p, s);
+    case 16: return launch_w4_columns<IN, 16>(p, s);
+    case 32: return launch_w4_columns<IN, 32>(p, s);
+    case 48: return launch_w4_columns<IN, 48>(p, s);
+    default: return launch_w4_columns<IN, 64>(p, s);
+  }
 }
 
 }  // namespace lsm
@@ -69,11 +79,13 @@ extern "C" int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const 
   if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return GEMM_ERR_UNSUPPORTED;
   if (lda >= kMaxLd || ldb >= kMaxLd || lds >= kMaxLd || ldz >= kMaxLd || ldc >= kMaxLd)
     return GEMM_ERR_UNSUPPORTED;
-  // groups of a power of two of at least 32, and whole 32s of K
   // 32-bit offsets inside a tile of 64 rows or columns
   if (K > 0 && (lda >= ((int64_t)1 << 24) || ldb >= ((int64_t)1 << 25))) return GEMM_ERR_UNSUPPORTED;
+  // groups of a power of two of at least 32, and whole 32s of K
   if (group < 32 || (group & (group - 1)) || group > kMaxDim || K % 32) return GEMM_ERR_UNSUPPORTED;
-  if (ceil_div(M, 16) * ceil_div(N, 16) >= ((int64_t)1 << 31)) return GEMM_ERR_UNSUPPORTED;
+  // a launch holds fewer than 2^32 threads
+  if (w4_row_tiles(M) * ceil_div(N, 16 * w4_column_blocks(M, N)) * 64 * w4_waves(K) >= ((int64_t)1 << 32))
+    return GEMM_ERR_UNSUPPORTED;
   if ((uintptr_t)C & (out_f32 ? 3 : 1)) return GEMM_ERR_UNSUPPORTED;
   if (K > 0 && (((uintptr_t)A & 15) || ((uintptr_t)B & 15) || ((uintptr_t)S & 1) || lda % 8 || ldb % 32))
     return GEMM_ERR_UNSUPPORTED;
