@@ -426,7 +426,10 @@ __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsW4<AR, NT>::WAVES_PER_SI
     // Loads stay where they are, a quarter before each k step: all of them at
     // once would hold the wave at the address queue, and left to itself the
     // compiler moves them behind the products.
-    __builtin_amdgcn_sched_barrier(0x386);   // VALU, SALU and LDS instructions may cross
+    if constexpr (NT == 4)
+      __builtin_amdgcn_sched_barrier(0x006);   // VALU and SALU instructions may cross: more would not fit the registers
+    else
+      __builtin_amdgcn_sched_barrier(0x386);   // and LDS instructions
   };
 
   v4f32 acc[RB][NT];

@@ -107,12 +107,13 @@ static hipError_t launch_rows_out(const Args &a, int dtype, hipStream_t s, const
   }
 }
 
-// Column blocks by M and N: two if that still makes a workgroup for every CU;
-// one where at most 8 rows make the activations' share small (1 x 16384 x 8192:
-// 23.6 us with one, 25.7 with two).
+// Column blocks: two if tiles of one would be more than the 256 CUs (measured
+// with one and two: 48 x 4608 x 4096 9.8 and 8.4 us, 16 x 4608 x 4096 6.5 and
+// 6.0; but 64 x 4096 x 4096 7.9 and 9.6); one where at most 8 rows make the
+// activations' share small (4 x 8192 x 8192: 12.5 us with one, 13.0 with two).
 template <int AR>
 static hipError_t dispatch_rows(const Args &a, int dtype, hipStream_t s, const RowColScale &sc) {
-  if (AR > 8 && ceil_div(a.M, AR < 16 ? 16 : AR) * ceil_div(a.N, 32) >= 256)
+  if (AR > 8 && ceil_div(a.M, AR < 16 ? 16 : AR) * ceil_div(a.N, 16) > 256)
     return launch_rows_out<AR, 2>(a, dtype, s, sc);
   return launch_rows_out<AR, 1>(a, dtype, s, sc);
 }

@@ -11,9 +11,13 @@ namespace lsm {
 
 // Rows of a tile, of which so many are loaded; waves of a workgroup: as many as
 // K has blocks for, up to eight (sixteen halve the registers, and took 16.2 us
-// for 1 x 16384 x 8192 where eight took 14.1); column blocks: two if that still
-// makes a workgroup for every CU (measured with one and two: 16 x 8192 x 8192
-// 12.0 and 10.6 us, 16 x 4096 x 4096 6.0 and 6.8).
+// for 1 x 16384 x 8192 where eight took 14.1); column blocks of 16: two if tiles
+// of one would be more than the 256 CUs, and from 17 to 48 rows four if tiles of
+// two would (64 rows by 64 columns do not fit the registers).  Measured with one
+// and two: 48 x 4608 x 4096 14.6 and 9.8 us, 16 x 4608 x 4096 7.0 and 6.2, one
+// row of it 6.2 and 5.8; but 48 x 4096 x 4096 8.8 and 10.5, 16 x 4096 x 4096 5.8
+// and 6.5.  With two and four: 48 x 8256 x 8192 31.5 and 26.3, 48 x 16384 x 8192
+// 40.2 and 32.3 (groups of 64), 32 x 16384 x 8192 29.0 and 24.4.
 static int w4_rows(int64_t M) { return M <= 4 ? 4 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : 64; }
 static int w4_waves(int64_t K) {
   int waves = 1;
@@ -24,7 +28,10 @@ static int64_t w4_row_tiles(int64_t M) {
   const int rows = w4_rows(M);
   return ceil_div(M, rows < 16 ? 16 : rows);
 }
-static int w4_column_blocks(int64_t M, int64_t N) { return w4_row_tiles(M) * ceil_div(N, 32) >= 256 ? 2 : 1; }
+static int w4_column_blocks(int64_t M, int64_t N) {
+  if (w4_row_tiles(M) * ceil_div(N, 16) <= 256) return 1;
+  return M > 16 && M <= 48 && ceil_div(N, 32) > 256 ? 4 : 2;
+}
 
 template <int IN, int AR, int NT, int GS>
 static hipError_t launch_w4(const W4Args &p, int waves, hipStream_t stream) {
@@ -47,7 +54,10 @@ static hipError_t launch_w4_group(const W4Args &p, hipStream_t s) {
 
 template <int IN, int AR>
 static hipError_t launch_w4_columns(const W4Args &p, hipStream_t s) {
-  if (w4_column_blocks(p.M, p.N) == 2) return launch_w4_group<IN, AR, 2>(p, s);
+  const int blocks = w4_column_blocks(p.M, p.N);
+  if constexpr (AR == 32 || AR == 48)
+    if (blocks == 4) return launch_w4_group<IN, AR, 4>(p, s);
+  if (blocks == 2) return launch_w4_group<IN, AR, 2>(p, s);
   return launch_w4_group<IN, AR, 1>(p, s);
 }
 

@@ -386,6 +386,15 @@ def test_w4_sizes(M, N, K):
         check_w4(M, N, K, 32 if N % 2 else 64, "bf16", "f32", N % 2 == 0, dist)
 
 
+@pytest.mark.parametrize("kind,out", [("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N", [(3, 4100), (16, 4100), (20, 4090), (20, 4100), (20, 8200), (48, 8260), (64, 4100)])
+def test_w4_column_blocks(kind, out, group, M, N):
+    """One, two and four blocks of 16 columns to a workgroup, several blocks of k to a wave."""
+    for dist in ("int", "real"):
+        check_w4(M, N, 1184, group, kind, out, M % 2 == 0, dist)
+
+
 @pytest.mark.parametrize("K", [32, 64, 96, 128, 160, 256, 512, 1984, 2048, 2080, 4096, 8192])
 def test_w4_lengths_of_k(K):
     for M in (1, 20, 64):
