@@ -221,12 +221,14 @@ __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsE4M3<AR, NT>::WAVES_PER_
 //    exponent, one shift and one and-or for two weights.  A 16-bit pair holds
 //    nibbles i and i + 4 of its dword, and the activations' pairs are permuted
 //    to match.
-//  * Zero point and scale.  In fp16 one packed subtraction makes q - z, exact
-//    for every byte z.  bf16 has no packed arithmetic: there sum a (q - z) =
-//    sum a (16 + q) - (16 + z) sum a, where sum a over the group comes from one
-//    more MFMA against ones, shared by the NT column blocks; both MFMA sums are
-//    of exact products, and |16 + q| <= 31 keeps what cancels within a few times
-//    the result's own rounding errors.  Then the group's sum is scaled in fp32.
+//  * Zero point and scale.  sum a (q - z) = sum a (16 + q) - (16 + z) sum a,
+//    where sum a over the group comes from one more MFMA against ones, shared
+//    by the NT column blocks; both MFMA sums are of exact products, and
+//    |16 + q| <= 31 keeps what cancels within a few times the result's own
+//    rounding errors.  In fp16 a packed subtraction makes q - z, exact for every
+//    byte z; it replaces the MFMAs against ones from 17 rows on (48 x 8192 x 8192,
+//    groups of 64: 19.7 and 17.7 us; but 16 x 8192 x 8192 9.5 and 10.2, where one
+//    such MFMA costs less).  Then the group's sum is scaled in fp32.
 //  * An infinite activation would turn a (16 + q) - (16 + z) a into a NaN, and
 //    a very large one might overflow there or before it meets a small scale,
 //    where the definition has a finite or infinite value: an entry that is not
@@ -379,6 +381,7 @@ __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsW4<AR, NT>::WAVES_PER_SI
   constexpr int RB = T::RB, LA = AR / 4;                // loads of A: 4 rows x 256 bytes, of B: 16 rows x 64
   constexpr int AROW = 2 * kRowsBlockK, BROW = kRowsBlockK / 2;
   constexpr int NG = 4 / GS;                            // scale groups in a block
+  constexpr bool SUB = IN == IN_F16 && RB > 1;          // q - z by subtraction
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int M = p.M, N = p.N, K = p.K;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
@@ -464,7 +467,7 @@ __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsW4<AR, NT>::WAVES_PER_SI
       w[t] = lane_group_transpose(*(const u32x4 *)(slice + kc_chunk_offset(16 * t + c, g, BROW)));
 #pragma unroll
     for (int gi = 0; gi < NG; gi++) {
-      v4f32 sum[RB], part[RB][NT];       // sum: bf16 only
+      v4f32 sum[RB], part[RB][NT];       // sum: unless SUB
 #pragma unroll
       for (int i = 0; i < RB; i++) {
         sum[i] = v4f32{0.f, 0.f, 0.f, 0.f};
@@ -482,12 +485,12 @@ __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsW4<AR, NT>::WAVES_PER_SI
           for (int i = 0; i < RB; i++) {
             const int row = AR >= 16 ? 16 * i + c : c & (AR - 1);
             fa[i] = *(const v8i16 *)(sa + kc_chunk_offset(row, 4 * j + g, AROW));
-            if constexpr (IN == IN_BF16) sum[i] = mfma_16x16x32<IN>(fa[i], ones, sum[i]);
+            if constexpr (!SUB) sum[i] = mfma_16x16x32<IN>(fa[i], ones, sum[i]);
           }
 #pragma unroll
           for (int t = 0; t < NT; t++) {
             v8i16 fb = w4_unpack<IN>(w[t][j], mask, base);
-            if constexpr (IN == IN_F16) fb = w4_minus_f16(fb, w4_zero_f16(v[t] >> 16));
+            if constexpr (SUB) fb = w4_minus_f16(fb, w4_zero_f16(v[t] >> 16));
 #pragma unroll
             for (int i = 0; i < RB; i++) part[i][t] = mfma_16x16x32<IN>(fa[i], fb, part[i][t]);
           }
@@ -501,7 +504,7 @@ __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsW4<AR, NT>::WAVES_PER_SI
           for (int i = 0; i < RB; i++)
 #pragma unroll
             for (int r = 0; r < 4; r++)
-              acc[i][t][r] += IN == IN_BF16 ? s * (part[i][t][r] - z * sum[i][r]) : s * part[i][t][r];
+              acc[i][t][r] += SUB ? s * part[i][t][r] : s * (part[i][t][r] - z * sum[i][r]);
         }
       }
     }
