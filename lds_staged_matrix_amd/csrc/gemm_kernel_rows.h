@@ -153,10 +153,11 @@ __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsE4M3<AR, NT>::WAVES_PER_
       if (past) a[i] = zero;
     }
   };
-  // operand of row r (of a slice part): the 32 bytes at k = 32 g
+  // operand of row r (of a slice part): the 16 bytes at k = 16 g and at 64 + 16 g
+  // (32 in a row would meet in banks two by two: lds_layout.h, frag16_kc8_offset)
   auto frag = [&](const char *part, int r) {
-    const u32x4 lo = *(const u32x4 *)(part + kc_chunk_offset(r, 2 * g, ROW));
-    const u32x4 hi = *(const u32x4 *)(part + kc_chunk_offset(r, 2 * g + 1, ROW));
+    const u32x4 lo = *(const u32x4 *)(part + kc_chunk_offset(r, g, ROW));
+    const u32x4 hi = *(const u32x4 *)(part + kc_chunk_offset(r, g + 4, ROW));
     return __builtin_bit_cast(v8i32, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
 
