@@ -50,7 +50,7 @@ static hipError_t launch_splitk_layout(const Args &a, int la, int lb, hipStream_
   return launch_splitk<MNC, MNC, IN, OUT, KS, NS>(a, s, sc);
 }
 
-// Products of at most 256 tiles of 64 x 64 (one for a CU) share each tile's K
+// Other products of at most 256 tiles of 64 x 64 (one for a CU) share each tile's K
 // out over groups of waves once it is 1024 long: two groups with four LDS
 // stages, or four with two for fp32 output, whose conversions want the waves.
 // Up to 1024 tiles and from K = 4096 on, two groups with two stages, so that
@@ -118,15 +118,17 @@ static hipError_t dispatch_rows(const Args &a, int dtype, hipStream_t s, const R
   return launch_rows_out<AR, 1>(a, dtype, s, sc);
 }
 
-// With both operands K-contiguous the few-rows kernel takes M <= 48, and up to
-// 192 rows while 64 x 64 tiles would fill no more than half of the CUs, each
-// walking all of K.  bf16 output, the few-rows kernel against the 64 x 64 tiles:
-// 33 x 16384 x 8192 31 and 35 us, 64 x 8192 x 8192 17 and 30, 128 x 4096 x 4096 11
-// and 17, 192 x 1152 x 896 5.0 and 5.4; but 64 x 16384 x 8192 43 and 36,
-// 128 x 8192 x 8192 36 and 32, 256 x 4096 x 4096 20 and 18.
+// With both operands K-contiguous the few-rows kernel takes M <= 32, and more
+// rows while its 64-row tiles, of one block of columns or of two, are at most
+// the 256 CUs: up to 64 tiles of 64 x 64, or up to 128 and K long enough for its
+// waves.  bf16 output, the few-rows kernel against the tiled ones: 64 x 4096 x
+// 4096 7.7 and 10.0 us, 1024 x 256 x 4096 7.1 and 9.7, 128 x 4096 x 4096 8.8 and
+// 9.9, 64 x 8192 x 8192 19.2 and 23.3 (fp32 output 19.8 and 30.5); but 128 x
+// 4096 x 896 6.2 and 5.6, 48 x 12288 x 4096 12.6 and 11.0, 128 x 8192 x 8192 33
+// and 23 (fp32 output 33 and 30).
 static bool few_rows(const Args &a, int la, int lb) {
-  return la == KC && lb == KC &&
-         (a.M <= 48 || (a.M <= 192 && ceil_div(a.M, 64) * ceil_div(a.N, 64) <= 128));
+  const int64_t tiles = ceil_div(a.M, 64) * ceil_div(a.N, 64);
+  return la == KC && lb == KC && (a.M <= 32 || tiles <= 64 || (tiles <= 128 && a.K >= 1536));
 }
 
 // Otherwise the split-K tiles where they pay, and the shape classes of

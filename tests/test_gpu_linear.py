@@ -256,6 +256,15 @@ def test_scaled_few_rows(M, N, K):
         check_scaled(M, N, K, KC, KC, "f32" if N % 2 else "bf16", dist, extra=N % 3)
 
 
+@pytest.mark.parametrize("M,N,K", [(260, 1000, 272), (1040, 200, 272), (4100, 47, 144), (250, 2000, 1552), (500, 1001, 2064),
+                                   (300, 600, 2048), (60, 8190, 1536)])
+@pytest.mark.parametrize("out", sorted(SCALED))
+def test_scaled_few_tiles(M, N, K, out):
+    """The few-rows kernel with many row tiles, one and two column blocks, cut in all extents."""
+    for dist in ("int", "real"):
+        check_scaled(M, N, K, KC, KC, out, dist, extra=M % 3)
+
+
 @pytest.mark.parametrize("M,N", [(201, 333), (1000, 1101)])
 @pytest.mark.parametrize("K", [1024, 1152, 1168, 4096, 4112, 4240])
 @pytest.mark.parametrize("out", ["f16", "f32"])
