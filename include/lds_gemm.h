@@ -145,9 +145,9 @@ int gemm_scaled_run(gemm_handle_t h, const void *A, const void *B, void *C,
  * carry a scale and a zero point for every `group` consecutive k:
  *     C[m][n] = round( sum_k A[m*lda + k] *
  *               S[(k/group)*lds + n] * (q(k,n) - Z[(k/group)*ldz + n]) )
- * summed in fp32, one rounding to C's type.  Meant for few rows (M <= 64: the
+ * summed in fp32, one rounding to C's type.  Meant for few rows (M <= 48: the
  * weights are read once); any M is computed, the weights being read again for
- * every 64 rows.
+ * every 32 or 48 rows.
  *   A            bf16/fp16, K-contiguous, 16-byte aligned; lda a multiple of 8.
  *   B            q(k,n) = bits 4*(k&1) .. 4*(k&1)+3 of byte (n*ldb + k)/2: two
  *                weights a byte, K-contiguous, even k in the low half.  16-byte

@@ -1,7 +1,7 @@
 // gemm_kernel_rows.h -- products of a few rows with a K-contiguous weight
 // matrix, for gfx950: E4M3 weights (scaled product) and 4-bit weights.
 //
-// With M <= 64 rows the product reads every weight once and does little with
+// With a few rows the product reads every weight once and does little with
 // it, so the time is the weights' bytes over the HBM rate, as long as enough
 // loads are in flight on every CU and nothing else takes longer.
 //  * A workgroup owns 16 * NT columns and 16 * RB rows of C; its waves split K
@@ -377,7 +377,7 @@ __device__ __forceinline__ void spread_rows(uint32_t (&out)[NT], uint32_t v) {
   }
 }
 
-// AR (4, 16, 32, 48 or 64): rows of A that are loaded; GS: k steps of 32 in a scale
+// AR (4, 16, 32 or 48): rows of A that are loaded; GS: k steps of 32 in a scale
 // group (4 stands for every group of 128 or more).
 template <int AR, int NT>
 struct RowsW4 {

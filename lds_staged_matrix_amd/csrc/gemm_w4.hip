@@ -9,16 +9,16 @@
 
 namespace lsm {
 
-// Rows of a tile, of which so many are loaded; waves of a workgroup: as many as
-// K has blocks for, up to eight (sixteen halve the registers, and took 16.2 us
-// for 1 x 16384 x 8192 where eight took 14.1); column blocks of 16: two if tiles
-// of one would be more than the 256 CUs, and from 17 to 48 rows four if tiles of
-// two would (64 rows by 64 columns do not fit the registers).  Measured with one
-// and two: 48 x 4608 x 4096 14.6 and 9.8 us, 16 x 4608 x 4096 7.0 and 6.2, one
-// row of it 6.2 and 5.8; but 48 x 4096 x 4096 8.8 and 10.5, 16 x 4096 x 4096 5.8
-// and 6.5.  With two and four: 48 x 8256 x 8192 31.5 and 26.3, 48 x 16384 x 8192
-// 40.2 and 32.3 (groups of 64), 32 x 16384 x 8192 29.0 and 24.4.
-static int w4_rows(int64_t M) { return M <= 4 ? 4 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : 64; }
+// Rows of a tile, of which so many are loaded: from 17 on 32 or 48, whichever
+// pads M less (128 x 8192 x 8192 39.4 us with 32 and 50.6 with 48; 192 rows, a tie,
+// 57.5 and 52.3; tiles of 64 rows, whose registers hold two column blocks at
+// most, took 42.8 and 62.6).
+static int w4_rows(int64_t M) {
+  if (M <= 16) return M <= 4 ? 4 : 16;
+  return ceil_div(M, 48) * 48 <= ceil_div(M, 32) * 32 ? 48 : 32;
+}
+// Waves of a workgroup: as many as K has blocks for, up to eight (sixteen halve
+// the registers, and took 16.2 us for 1 x 16384 x 8192 where eight took 14.1).
 static int w4_waves(int64_t K) {
   int waves = 1;
   while (2 * waves <= kRowsMaxWaves && 2 * waves * kRowsBlockK <= K) waves *= 2;
@@ -28,9 +28,15 @@ static int64_t w4_row_tiles(int64_t M) {
   const int rows = w4_rows(M);
   return ceil_div(M, rows < 16 ? 16 : rows);
 }
+// Column blocks of 16: two if tiles of one would be more than the 256 CUs, and
+// from 17 rows on four if tiles of two would.  Measured with one and two: 48 x
+// 4608 x 4096 14.6 and 9.8 us, 16 x 4608 x 4096 7.0 and 6.2, one row of it 6.2 and
+// 5.8; but 48 x 4096 x 4096 8.8 and 10.5, 16 x 4096 x 4096 5.8 and 6.5.  With two
+// and four: 48 x 8256 x 8192 31.5 and 26.3, 48 x 16384 x 8192 40.2 and 32.3
+// (groups of 64), 32 x 16384 x 8192 29.0 and 24.4.
 static int w4_column_blocks(int64_t M, int64_t N) {
   if (w4_row_tiles(M) * ceil_div(N, 16) <= 256) return 1;
-  return M > 16 && M <= 48 && ceil_div(N, 32) > 256 ? 4 : 2;
+  return M > 16 && w4_row_tiles(M) * ceil_div(N, 32) > 256 ? 4 : 2;
 }
 
 template <int IN, int AR, int NT, int GS>
@@ -55,7 +61,7 @@ static hipError_t launch_w4_group(const W4Args &p, hipStream_t s) {
 template <int IN, int AR>
 static hipError_t launch_w4_columns(const W4Args &p, hipStream_t s) {
   const int blocks = w4_column_blocks(p.M, p.N);
-  if constexpr (AR == 32 || AR == 48)
+  if constexpr (AR > 16)
     if (blocks == 4) return launch_w4_group<IN, AR, 4>(p, s);
   if (blocks == 2) return launch_w4_group<IN, AR, 2>(p, s);
   return launch_w4_group<IN, AR, 1>(p, s);
@@ -67,8 +73,7 @@ static hipError_t dispatch_w4(const W4Args &p, hipStream_t s) {
     case 4: return launch_w4_columns<IN, 4>(p, s);
     case 16: return launch_w4_columns<IN, 16>(p, s);
     case 32: return launch_w4_columns<IN, 32>(p, s);
-    case 48: return launch_w4_columns<IN, 48>(p, s);
-    default: return launch_w4_columns<IN, 64>(p, s);
+    default: return launch_w4_columns<IN, 48>(p, s);
   }
 }
 

@@ -108,7 +108,7 @@ W4_CASES = [
     (dict(lds=1 << 40), UNSUPPORTED), (dict(ldz=1 << 40), UNSUPPORTED), (dict(ldc=1 << 40), UNSUPPORTED),
     (dict(M=(1 << 30) - 1, N=(1 << 30) - 1, lds=1 << 30, ldz=1 << 30, ldc=1 << 30), UNSUPPORTED),
     (dict(M=1 << 29, ldc=(1 << 39)), UNSUPPORTED),
-    # 2^32 threads: tiles of 64 x 32 by eight waves from K = 1024 on, by one wave below 256
+    # 2^32 threads: tiles of 32 x 64 by eight waves from K = 1024 on, by one wave below 256
     (dict(A=1 << 40, B=1 << 44, S=1 << 48, Z=1 << 49, C=1 << 50, M=1 << 17, N=1 << 17, K=1024, lda=1024, ldb=1024,
           lds=1 << 17, ldz=1 << 17, ldc=1 << 17), UNSUPPORTED),
     (dict(A=1 << 40, B=1 << 44, S=1 << 48, Z=1 << 49, C=1 << 50, M=1 << 17, N=1 << 16, K=1024, lda=1024, ldb=1024,
