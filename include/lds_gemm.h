@@ -178,7 +178,8 @@ int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const void *S,
  *     Y[m*ldy + n] = y[m][n] / S[m] rounded to E4M3,
  * so that S and Y are the SA and A of gemm_scaled_run.  All arithmetic is
  * fp32, the squares included (rows whose squares' sum overflows there give
- * zeros), and y is computed from h before it is rounded.  A NaN in a row makes
+ * zeros; with eps == 0, rows whose squares all vanish there give NaN and
+ * infinities), and y is computed from h before it is rounded.  A NaN in a row makes
  * all of its y NaN; an infinity is NaN at its place and makes the others zero;
  * with E4M3 output either one makes the row and S[m] NaN.
  *   X, R, W, H   elements of the input type, 2-byte aligned; R and H may be

@@ -10,7 +10,9 @@
 // the HBM rate is the bound, and with one row the latency of a load, a
 // reduction and a store.  A row stays in the registers of the threads that
 // own it: max |y| is max |h w| over the root, so the sum of squares and the
-// maximum come out of one reduction and nothing is read again.
+// maximum come out of one reduction and nothing is read again.  Where max |h w|
+// leaves fp32's normal range, which max |y| need not do, the maximum is taken
+// again over y itself.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -130,20 +132,19 @@ __device__ __forceinline__ void store_chunk8(uint8_t *at, const float (&v)[kChun
   __builtin_memcpy(at, &d, sizeof(d));
 }
 
-// The root's reciprocal and, for E4M3 output, 448 / max |y| (and the scale,
-// stored by the row's first thread).
-template <bool Q8>
-__device__ __forceinline__ void row_factors(const NormArgs &p, int64_t m, int t, float sum, uint32_t top,
-                                            float &root, float &inv) {
-  root = rsqrtf(sum / (float)p.N + p.eps);
-  inv = 1.f;
-  if constexpr (Q8) {
-    float amax = root * __builtin_bit_cast(float, top);
-    amax = amax < kAmaxMin ? kAmaxMin : amax;              // a NaN stays
-    inv = kE4M3Max / amax;
-    if (t == 0) p.S[m] = amax / kE4M3Max;
-  }
+// The scale of an E4M3 row (stored by the row's first thread) and its
+// reciprocal, 448 / max |y|.
+__device__ __forceinline__ float row_scale(const NormArgs &p, int64_t m, int t, float amax) {
+  amax = amax < kAmaxMin ? kAmaxMin : amax;                // a NaN stays
+  if (t == 0) p.S[m] = amax / kE4M3Max;
+  return kE4M3Max / amax;
 }
+
+// Whether max |h w| lies in fp32's normal range and max |y| is its product with
+// the root.  Otherwise (zero, subnormal, infinite or NaN; alike in all of a
+// row's threads) `top` is to be max |y|: y is h times the root, which is at most
+// sqrt(N), times w, and overflows only where the formula does.
+__device__ __forceinline__ bool in_normal_range(uint32_t top) { return top - 0x00800000u < 0x7F000000u; }
 
 // A row's chunk c of eight elements starts at 8 c; the last one, if the row is
 // no multiple of eight, is moved back to end with the row, and its first `skip`
@@ -181,6 +182,17 @@ __device__ __forceinline__ void take_chunk(const NormArgs &p, int64_t m, const C
       if (i >= c.skip) all += h[i] * h[i];
   }
   sum += all;
+}
+
+// max |y| of a chunk, as bits.
+__device__ __forceinline__ uint32_t top_of_y(const float (&h)[kChunk], const float (&w)[kChunk], float root) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kChunk; i++) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, h[i] * root * w[i]) & 0x7FFFFFFFu;
+    top = b > top ? b : top;
+  }
+  return top;
 }
 
 template <int IN, bool Q8>
@@ -223,8 +235,24 @@ __global__ __launch_bounds__(ROWS > 1 ? 64 * ROWS : 1024) void rmsnorm_kernel(co
     wave_sum_max(sum, top);
   else
     row_sum_max(sum, top, threads >> 6);
-  float root, inv;
-  row_factors<Q8>(p, m, t, sum, top, root, inv);
+  const float root = rsqrtf(sum / (float)p.N + p.eps);
+  float inv = 1.f;
+  if constexpr (Q8) {
+    float amax = root * __builtin_bit_cast(float, top);
+    if (!in_normal_range(top)) {
+      top = 0;
+#pragma unroll
+      for (int v = 0; v < V; v++) top = max(top, top_of_y(h[v], w[v], root));
+      if constexpr (ROWS > 1) {
+        wave_sum_max(sum, top);
+      } else {
+        __syncthreads();                 // every wave has read the first reduction
+        row_sum_max(sum, top, threads >> 6);
+      }
+      amax = __builtin_bit_cast(float, top);
+    }
+    inv = row_scale(p, m, t, amax);
+  }
 #pragma unroll
   for (int v = 0; v < V; v++) finish_chunk<IN, Q8>(p, m, Chunk(t + v * threads, p.N), h[v], w[v], root, inv);
 }
@@ -253,8 +281,25 @@ __global__ __launch_bounds__(1024) void rmsnorm_any_kernel(const NormArgs p) {
     top = b > top ? b : top;
   }
   row_sum_max(sum, top, blockDim.x >> 6);
-  float root, inv;
-  row_factors<Q8>(p, m, threadIdx.x, sum, top, root, inv);
+  const float root = rsqrtf(sum / (float)p.N + p.eps);
+  float inv = 1.f;
+  if constexpr (Q8) {
+    float amax = root * __builtin_bit_cast(float, top);
+    if (!in_normal_range(top)) {
+      float none = 0.f;
+      top = tail < p.N ? __builtin_bit_cast(uint32_t, ht * root * wt) & 0x7FFFFFFFu : 0;
+      for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+        float h[kChunk], w[kChunk];
+        uint32_t unused = 0;
+        take_chunk<IN>(p, m, Chunk(c, p.N), h, w, none, unused);
+        top = max(top, top_of_y(h, w, root));
+      }
+      __syncthreads();                   // every wave has read the first reduction
+      row_sum_max(none, top, blockDim.x >> 6);
+      amax = __builtin_bit_cast(float, top);
+    }
+    inv = row_scale(p, m, threadIdx.x, amax);
+  }
   for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
     float h[kChunk], w[kChunk];
     take_chunk<IN>(p, m, Chunk(c, p.N), h, w, sum, top);

@@ -1,0 +1,58 @@
+"""The linear-layer operators where values meet the ends of their types' ranges,
+against the fp64 definitions of linear_reference.py."""
+import numpy as np
+import pytest
+import torch
+
+import gpu_harness as H
+import lds_staged_matrix_amd as lsm
+import linear_reference as R
+import test_gpu_linear as T
+
+pytestmark = pytest.mark.gpu
+
+# rows by waves, one, two and four chunks a thread, rows read twice (with and without whole chunks)
+NORM_LENGTHS = [256, 1031, 16384, 20000, 40003, 5]
+
+
+def norm(x, w, eps, kind, out):
+    """(Y, S) in fp64."""
+    M, N = x.shape
+    X, W = T.padded(x, N, kind), T.padded(w, N, kind)
+    Y, S = T.Out(M, N, N, out), T.Out(1, M, M, "f32")
+    print("CASE norm range", M, N, kind, out, eps, flush=True)
+    T.ok(lsm.gemm_rmsnorm_run(H.handle(), X, None, W, None, Y.view, S.view, M, N, N, 0, 0, N, eps,
+                              T.NORM[kind, out], torch.cuda.current_stream()), "gemm_rmsnorm_run")
+    Y.check("Y")
+    S.check("S")
+    return R.f64(Y.view), R.f64(S.view)[0]
+
+
+@pytest.mark.parametrize("N", NORM_LENGTHS)
+@pytest.mark.parametrize("rows,weight,eps", [((1e15, 1e10, 1.0), 3e24, 1e-5), ((1e-18, 1e-10, 1.0), 1e-28, 0.0),
+                                             ((1e-18, 1e-10, 1.0), 1e-25, 0.0)])
+def test_norm_whose_products_leave_the_range(N, rows, weight, eps):
+    """h w overflows or is subnormal, or vanishes, in some rows; y = h w / root is an ordinary number in all."""
+    rng = np.random.default_rng(N)
+    x = R.round_to(rng.standard_normal((len(rows), N)) * np.array(rows)[:, None], "bf16")
+    w = R.round_to((1 + 0.25 * rng.standard_normal((1, N))) * weight, "bf16")
+    _, y = R.rmsnorm(x, None, w, eps)
+    for out in ("e4m3", "bf16"):
+        Y, S = norm(x, w, eps, "bf16", out)
+        T.check_norm(len(rows), N, "bf16", out, (None, y, None, Y, S))
+
+
+@pytest.mark.parametrize("N", NORM_LENGTHS)
+def test_norm_whose_squares_overflow(N):
+    """Rows of finite values whose squares' sum overflows fp32 give zeros, whatever h w does; the others
+    are untouched."""
+    x = np.ones((4, N))
+    x[0], x[1], x[2, N - 1] = 3e38, 1e20, -3e38
+    x, w = R.round_to(x, "bf16"), np.full((1, N), 2.0)
+    for out in ("e4m3", "bf16"):
+        Y, S = norm(x, w, 1e-5, "bf16", out)
+        assert (Y[:3] == 0).all()
+        if out == "e4m3":
+            assert (S[:3] == np.float32(2.0 ** -100) / np.float32(448)).all()
+        _, y = R.rmsnorm(x[3:], None, w, 1e-5)
+        T.check_norm(1, N, "bf16", out, (None, y, None, Y[3:], S[3:]))
