@@ -163,6 +163,11 @@ def _lib():
     return _library
 
 
+def _stream():
+    """The stream that the inputs were made on and the outputs are read on."""
+    return torch.cuda.current_stream()
+
+
 def _check(lsm, status, what):
     if status != lsm.GEMM_OK:
         raise lsm.GemmError(status, what)
@@ -175,7 +180,8 @@ def _own_norm(s):
              ("f16", "f16"): lsm.GEMM_NORM_F16_F16, ("f16", "e4m3"): lsm.GEMM_NORM_F16_E4M3}[s["type"], s["out"]]
     _check(lsm, lsm.gemm_rmsnorm_run(h, X, R, s["W"], H, Y, s["S"], s["M"], s["N"], X.stride(0),
                                      R.stride(0) if R is not None else 0,
-                                     H.stride(0) if H is not None else 0, Y.stride(0), EPS, dtype),
+                                     H.stride(0) if H is not None else 0, Y.stride(0), EPS, dtype,
+                                     _stream()),
            "gemm_rmsnorm_run")
     return {"Y": Y, "S": s["S"], "H": H}
 
@@ -186,7 +192,7 @@ def _own_scaled(s):
     dtype = {"bf16": lsm.GEMM_E4M3_BF16, "f16": lsm.GEMM_E4M3_F16, "f32": lsm.GEMM_E4M3_F32}[s["out"]]
     _check(lsm, lsm.gemm_scaled_run(h, A, B, C, s["SA"], s["SB"], s["M"], s["N"], s["K"], A.stride(0),
                                     B.stride(0), C.stride(0), 1, 1, lsm.GEMM_K_CONTIG,
-                                    lsm.GEMM_K_CONTIG, dtype),
+                                    lsm.GEMM_K_CONTIG, dtype, _stream()),
            "gemm_scaled_run")
     return C
 
@@ -198,7 +204,7 @@ def _own_w4(s):
              ("f16", "f16"): lsm.GEMM_F16_F16, ("f16", "f32"): lsm.GEMM_F16_F32}[s["type"], s["out"]]
     _check(lsm, lsm.gemm_w4_run(h, A, B, S, Z, C, s["M"], s["N"], s["K"], s["group"], A.stride(0),
                                 2 * B.stride(0), S.stride(0), Z.stride(0) if Z is not None else 0,
-                                C.stride(0), dtype),
+                                C.stride(0), dtype, _stream()),
            "gemm_w4_run")
     return C
 
