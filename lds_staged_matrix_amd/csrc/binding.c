@@ -5,7 +5,8 @@
  * on the host; the same call through ctypes added 1.6 us of marshalling, this
  * adds 0.4.  Arguments are taken by position, as the package's functions of the
  * same names pass them:
- *   handle   a ctypes.c_void_p, an integer or None
+ *   handle   what a ctypes.c_void_p parameter takes (a c_void_p, an integer, None);
+ *            anything else raises ctypes.ArgumentError
  *   pointers integers, None, or objects with a data_ptr() method
  *   integers anything int() takes; one that its C parameter cannot hold raises
  *            OverflowError
@@ -25,6 +26,7 @@ static __typeof__(gemm_scaled_run) *p_scaled;
 static __typeof__(gemm_w4_run) *p_w4;
 static __typeof__(gemm_rmsnorm_run) *p_rmsnorm;
 static PyObject *s_data_ptr, *s_cuda_stream, *s_value;
+static PyObject *c_void_p, *c_cast;                 /* of ctypes */
 
 /* int(x) as an address; the low 64 bits count. */
 static int int_address(PyObject *x, void **out) {
@@ -52,6 +54,25 @@ static int address(PyObject *x, PyObject *name, int call, void **out) {
     if (!r) return -1;
     v = r;
   }
+  const int e = v == Py_None ? 0 : int_address(v, out);
+  Py_DECREF(v);
+  return e;
+}
+
+/* A handle's address.  The library reads what it points to, so nothing is taken
+ * for one that ctypes would not convert to a pointer: no float, no number of
+ * another library, no object that merely has a value. */
+static int handle(PyObject *x, void **out) {
+  *out = NULL;
+  if (x == Py_None) return 0;
+  if (PyLong_Check(x)) return int_address(x, out);
+  const int is = PyObject_IsInstance(x, c_void_p);
+  if (is < 0) return -1;
+  PyObject *p = is ? Py_NewRef(x) : PyObject_CallFunctionObjArgs(c_cast, x, c_void_p, NULL);
+  if (!p) return -1;
+  PyObject *v = PyObject_GetAttr(p, s_value);
+  Py_DECREF(p);
+  if (!v) return -1;
   const int e = v == Py_None ? 0 : int_address(v, out);
   Py_DECREF(v);
   return e;
@@ -96,7 +117,7 @@ static int take(const struct shape *t, PyObject *const *a, Py_ssize_t n, struct 
     return -1;
   }
   void *x;
-  if (address(*a++, s_value, 0, &x)) return -1;
+  if (handle(*a++, &x)) return -1;
   v->h = (gemm_handle_t)x;
   for (int i = 0; i < t->np; i++)
     if (address(*a++, s_data_ptr, 1, &v->p[i])) return -1;
@@ -195,5 +216,11 @@ PyMODINIT_FUNC PyInit__binding(void) {
   s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
   s_value = PyUnicode_InternFromString("value");
   if (!s_data_ptr || !s_cuda_stream || !s_value) return NULL;
+  PyObject *ctypes = PyImport_ImportModule("ctypes");
+  if (!ctypes) return NULL;
+  c_void_p = PyObject_GetAttrString(ctypes, "c_void_p");
+  c_cast = PyObject_GetAttrString(ctypes, "cast");
+  Py_DECREF(ctypes);
+  if (!c_void_p || !c_cast) return NULL;
   return PyModule_Create(&module);
 }

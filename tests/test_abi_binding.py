@@ -1,0 +1,65 @@
+"""What the binding takes for a handle, and what it is built on (CPU; no call
+below passes the device check)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import lds_staged_matrix_amd as lsm
+from test_abi_linear import FAKE, NORM, SCALED, VALID, W4, _FAKE_DEVICE, addr, lib  # noqa: F401
+
+RUN = dict(A=addr(0), B=addr(1), C=addr(2), M=16, N=16, K=16, lda=16, ldb=16, ldc=16, layoutA=0, layoutB=0,
+           dtype=lsm.GEMM_BF16_F32)
+ENTRIES = [(lsm.gemm_run, RUN), (lsm.gemm_scaled_run, SCALED), (lsm.gemm_w4_run, W4), (lsm.gemm_rmsnorm_run, NORM)]
+ADDRESS = ctypes.addressof(_FAKE_DEVICE)           # below 2^53: a float holds it
+
+
+class Valued:
+    value = ADDRESS
+
+
+class Numbered:
+    def __int__(self):
+        return ADDRESS
+    __index__ = __int__
+
+
+class AsParameter:
+    _as_parameter_ = FAKE
+
+
+class Handle(ctypes.c_void_p):
+    pass
+
+
+def ids(entries):
+    return [fn.__name__ for fn, _ in entries]
+
+
+@pytest.mark.parametrize("fn,base", ENTRIES, ids=ids(ENTRIES))
+@pytest.mark.parametrize("handle", [float(ADDRESS), np.int64(ADDRESS), np.array([ADDRESS]), ctypes.c_int64(ADDRESS),
+                                    Valued(), Numbered()], ids=lambda h: type(h).__name__)
+def test_no_handle(fn, base, handle):
+    with pytest.raises(ctypes.ArgumentError):
+        fn(handle, **base)
+
+
+@pytest.mark.parametrize("fn,base", ENTRIES, ids=ids(ENTRIES))
+@pytest.mark.parametrize("handle", [FAKE, ADDRESS, ADDRESS + (1 << 64), Handle(ADDRESS),
+                                    ctypes.pointer(_FAKE_DEVICE), ctypes.byref(_FAKE_DEVICE), AsParameter()],
+                         ids=lambda h: type(h).__name__)
+def test_handles(fn, base, handle):
+    """What a ctypes c_void_p parameter takes."""
+    assert fn(handle, **base) == VALID
+
+
+@pytest.mark.parametrize("fn,base", ENTRIES, ids=ids(ENTRIES))
+@pytest.mark.parametrize("handle", [None, 0, ctypes.c_void_p()], ids=str)
+def test_null_handles(fn, base, handle):
+    assert fn(handle, **base) == lsm.GEMM_ERR_INVALID_ARG
+
+
+def test_a_tensor_is_no_handle():
+    torch = pytest.importorskip("torch")
+    with pytest.raises(ctypes.ArgumentError):
+        lsm.gemm_run(torch.tensor(ADDRESS), **RUN)
