@@ -14,7 +14,9 @@
  * and the gemm_status comes back.  bind() takes the addresses of the entry
  * points in the loaded library.
  */
-#define PY_SSIZE_T_CLEAN
+/* The stable ABI from Python 3.10 on, the oldest that torch's ROCm builds serve:
+ * one build loads in every later Python. */
+#define Py_LIMITED_API 0x030A0000
 #include <Python.h>
 
 #include <stdint.h>
@@ -222,5 +224,10 @@ PyMODINIT_FUNC PyInit__binding(void) {
   c_cast = PyObject_GetAttrString(ctypes, "cast");
   Py_DECREF(ctypes);
   if (!c_void_p || !c_cast) return NULL;
-  return PyModule_Create(&module);
+  PyObject *m = PyModule_Create(&module);
+  if (m && PyModule_AddIntConstant(m, "limited_api", Py_LIMITED_API) < 0) {
+    Py_DECREF(m);
+    return NULL;
+  }
+  return m;
 }

@@ -1,6 +1,8 @@
 """What the binding takes for a handle, and what it is built on (CPU; no call
 below passes the device check)."""
 import ctypes
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -63,3 +65,19 @@ def test_a_tensor_is_no_handle():
     torch = pytest.importorskip("torch")
     with pytest.raises(ctypes.ArgumentError):
         lsm.gemm_run(torch.tensor(ADDRESS), **RUN)
+
+
+def test_one_build_for_every_python():
+    """The binding is compiled against the stable ABI: of Python's own symbols it asks for documented
+    functions only, and reads none of its objects' fields."""
+    from lds_staged_matrix_amd import _binding
+    assert _binding.limited_api == 0x030A0000
+    nm = shutil.which("nm")
+    if nm is None:
+        pytest.skip("no nm")
+    out = subprocess.run([nm, "-D", "--undefined-only", _binding.__file__], capture_output=True, text=True, check=True)
+    names = {line.split()[-1] for line in out.stdout.splitlines() if "Py" in line}
+    assert "PyLong_FromLong" in names
+    # what the stable ABI's own macros expand to
+    assert {n for n in names if n.startswith("_Py")} <= {"_Py_Dealloc", "_Py_NoneStruct"}
+    assert "PyType_GetFlags" in names          # PyLong_Check through a call, not through the type's fields
