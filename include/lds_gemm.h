@@ -78,6 +78,10 @@ enum gemm_dtype {
     GEMM_E4M3_F16 = 6    /* fp8 E4M3 A, B;  fp16 C: gemm_scaled_run only   */
 };
 
+/* Added to gemm_scaled_run's dtype: sums of exact products in fp32 for 16-bit
+ * output too, at up to twice the time (fp32 output always has them). */
+enum { GEMM_EXACT_SUMS = 0x100 };
+
 /* Element types of gemm_rmsnorm_run, named input_output. */
 enum gemm_norm_dtype {
     GEMM_NORM_BF16_BF16 = 0,
@@ -123,15 +127,20 @@ int gemm_run(gemm_handle_t h, const void *A, const void *B, void *C,
 /* Enqueue C <- diag(SA) * A * B * diag(SB) on `stream`, for E4M3 operands:
  *     C[m][n] = round( (sum_k a(m,k) * b(k,n)) * SA[m*incA] * SB[n*incB] )
  * with the sum in fp32, the two factors applied to it in fp32 in that order,
- * and one rounding to C's type.  For fp32 output, and for M <= 32, the sum is
- * one of exact products in fp32.  For 16-bit output of more rows the fp8 matrix
- * instruction may make it, which aligns eight products at a time to the largest
- * and drops what lies 13 bits or more below: at most 2^-10 sum |a b| is lost,
- * 1.5e-5 of the result on ordinary data, a hundredth of a bf16 rounding.
+ * and one rounding to C's type.  For fp32 output, for M <= 32 and where dtype
+ * has GEMM_EXACT_SUMS, the sum is one of exact products in fp32.  For 16-bit
+ * output of more rows the fp8 matrix instruction may make it, which takes eight
+ * products at a time, aligns them to the largest and drops what lies 13 bits or
+ * more below (the sum so far is not aligned to them and keeps fp32's bits): at
+ * most 7 * 2^-13 of a group's largest product is lost, 2^-10 sum |a b| in all;
+ * 1.5e-5 of the result on normal data and 5e-5 where one k in a hundred is twenty
+ * times louder, against 1.7e-3 (bf16) or 2e-4 (fp16) of the output's rounding.
+ * A sum of which large products cancel may lose all of a small result to it.
  *   SA, SB       device pointers to fp32 scales, 4-byte aligned: one for each
  *                row of A and each column of B (incA, incB = 1), or one for
  *                all of them (0).  They must not overlap C.
- *   dtype        GEMM_E4M3_F32, GEMM_E4M3_BF16 or GEMM_E4M3_F16.
+ *   dtype        GEMM_E4M3_F32, GEMM_E4M3_BF16 or GEMM_E4M3_F16, or one of them
+ *                + GEMM_EXACT_SUMS.
  * Everything else is as for gemm_run with E4M3 operands, K == 0 included: the
  * empty sum is scaled like any other. */
 int gemm_scaled_run(gemm_handle_t h, const void *A, const void *B, void *C,

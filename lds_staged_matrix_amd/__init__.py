@@ -20,7 +20,7 @@ import os
 __all__ = [
     "GEMM_K_CONTIG", "GEMM_MN_CONTIG",
     "GEMM_BF16_F32", "GEMM_BF16_BF16", "GEMM_F16_F16", "GEMM_F16_F32", "GEMM_E4M3_F32",
-    "GEMM_E4M3_BF16", "GEMM_E4M3_F16",
+    "GEMM_E4M3_BF16", "GEMM_E4M3_F16", "GEMM_EXACT_SUMS",
     "GEMM_NORM_BF16_BF16", "GEMM_NORM_BF16_E4M3", "GEMM_NORM_F16_F16", "GEMM_NORM_F16_E4M3",
     "GEMM_OK", "GEMM_ERR_INVALID_ARG", "GEMM_ERR_UNSUPPORTED", "GEMM_ERR_DEVICE",
     "GEMM_ERR_LAUNCH", "GemmError", "library_path", "load_library", "gemm_create",
@@ -31,6 +31,7 @@ __all__ = [
 GEMM_K_CONTIG, GEMM_MN_CONTIG = 0, 1
 GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_F16_F16, GEMM_F16_F32 = 0, 1, 2, 3
 GEMM_E4M3_F32, GEMM_E4M3_BF16, GEMM_E4M3_F16 = 4, 5, 6
+GEMM_EXACT_SUMS = 0x100     # added to gemm_scaled_run's dtype
 GEMM_NORM_BF16_BF16, GEMM_NORM_BF16_E4M3, GEMM_NORM_F16_F16, GEMM_NORM_F16_E4M3 = range(4)
 GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED, GEMM_ERR_DEVICE, GEMM_ERR_LAUNCH = range(5)
 EXPORTED_SYMBOLS = ("gemm_create", "gemm_run", "gemm_scaled_run", "gemm_w4_run", "gemm_rmsnorm_run",

@@ -102,7 +102,8 @@ __device__ __forceinline__ void store_rows(void *C, int64_t idx, float v) {
 //
 // C[m][n] = sum_k a(m,k) b(k,n) * sc.a[m] * sc.b[n], both operands
 // K-contiguous, K a multiple of 16.  AR (8, 16, 32, 48 or 64): rows of A that
-// are loaded.
+// are loaded.  IN: IN_E4M3 (fp8 MFMAs) or IN_E4M3_AS_BF16 (exact products, fp32
+// sums).
 template <int AR, int NT>
 struct RowsE4M3 {
   static constexpr int RB = AR <= 16 ? 1 : AR / 16;
@@ -110,7 +111,7 @@ struct RowsE4M3 {
   static constexpr int WAVES_PER_SIMD = RB <= 2 ? 4 : 2;   // 128 registers a lane, or 256
 };
 
-template <int AR, int NT, int OUT>
+template <int AR, int NT, int IN, int OUT>
 __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsE4M3<AR, NT>::WAVES_PER_SIMD)) void lds_gemm_rows_e4m3_kernel(
     const char *__restrict__ A, const char *__restrict__ B, void *__restrict__ C, int M, int N, int K,
     uint32_t lda, uint32_t ldb, int64_t ldc, int tiles_m, RowColScale sc) {
@@ -181,10 +182,7 @@ __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsE4M3<AR, NT>::WAVES_PER_
     for (int i = 0; i < RB; i++) fa[i] = frag(sa, AR >= 16 ? 16 * i + c : c & (AR - 1));
 #pragma unroll
     for (int t = 0; t < NT; t++) fb[t] = frag(slice, 16 * t + c);
-    // From 33 rows on 16-bit outputs take the fp8 MFMA (128 x 4096 x 4096 9.7 and
-    // 8.7 us, 192 x 2048 x 8192 14.5 and 12.0); with fewer HBM is the bound and
-    // the exact form costs nothing.
-    if constexpr (RB >= 3 && OUT != OUT_F32) {
+    if constexpr (IN == IN_E4M3) {
 #pragma unroll
       for (int i = 0; i < RB; i++)
 #pragma unroll

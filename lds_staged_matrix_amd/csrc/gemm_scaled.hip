@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "gemm_kernel_rows.h"
 #include "gemm_kernel_splitk.h"
@@ -13,17 +14,35 @@
 
 namespace lsm {
 
+// What is asked for: the output's type, and whether the sums are to be exact.
 // An fp32 output multiplies its operands as bf16, whose MFMAs sum in fp32
-// throughout (see e4m3_part_as_bf16); 16-bit outputs, rounded to 2^-8 or 2^-11,
-// take the fp8 MFMAs at twice the rate -- except where HBM is the bound anyway
-// (few rows, IN16).
+// throughout (see e4m3_part_as_bf16).  A 16-bit output, whose rounding is off by
+// up to 2^-8 or 2^-11, takes the fp8 MFMAs at twice the rate, unless the caller
+// asks for exact sums (GEMM_EXACT_SUMS) or HBM is the bound anyway (few rows).
+struct Wanted {
+  int out;
+  bool exact;
+};
+
+// call(IN, OUT) with the element types as constants; IN16: of 16-bit outputs
+// that need no exact sums.
+template <int IN16, class F>
+static hipError_t with_types(const Wanted &w, F call) {
+  constexpr std::integral_constant<int, IN_E4M3_AS_BF16> exact{};
+  constexpr std::integral_constant<int, IN16> fast{};
+  constexpr std::integral_constant<int, OUT_F32> f32{};
+  constexpr std::integral_constant<int, OUT_BF16> bf16{};
+  constexpr std::integral_constant<int, OUT_F16> f16{};
+  if (w.out == OUT_F32) return call(exact, f32);
+  if (w.out == OUT_BF16) return w.exact ? call(exact, bf16) : call(fast, bf16);
+  return w.exact ? call(exact, f16) : call(fast, f16);
+}
+
 template <class T, int KIND, int IN16 = IN_E4M3>
-static hipError_t launch_scaled(const Args &a, int la, int lb, int dtype, hipStream_t s, const RowColScale &sc) {
-  switch (dtype) {
-    case GEMM_E4M3_F32: return launch_layout<T, KIND, IN_E4M3_AS_BF16, OUT_F32, RowColScale>(a, la, lb, s, sc);
-    case GEMM_E4M3_BF16: return launch_layout<T, KIND, IN16, OUT_BF16, RowColScale>(a, la, lb, s, sc);
-    default: return launch_layout<T, KIND, IN16, OUT_F16, RowColScale>(a, la, lb, s, sc);
-  }
+static hipError_t launch_scaled(const Args &a, int la, int lb, const Wanted &w, hipStream_t s, const RowColScale &sc) {
+  return with_types<IN16>(w, [&](auto in, auto out) {
+    return launch_layout<T, KIND, decltype(in)::value, decltype(out)::value, RowColScale>(a, la, lb, s, sc);
+  });
 }
 
 template <int LA, int LB, int IN, int OUT, int KS, int NS>
@@ -52,7 +71,7 @@ static hipError_t launch_splitk_layout(const Args &a, int la, int lb, hipStream_
 
 // Other products of at most 256 tiles of 64 x 64 (one for a CU) share each tile's K
 // out over groups of waves once it is 1024 long: two groups with four LDS
-// stages, or four with two for fp32 output, whose conversions want the waves.
+// stages, or four with two for exact sums, whose conversions want the waves.
 // Up to 1024 tiles and from K = 4096 on, two groups with two stages, so that
 // two workgroups fit a CU.  Kernel times against the kernels without the split:
 //   bf16 output  256 x 4096 x 4096 12.2 and 18.2 us, 256 x 2048 x 8192 16.9 and
@@ -62,25 +81,24 @@ static hipError_t launch_splitk_layout(const Args &a, int la, int lb, hipStream_
 //   fp32 output  256 x 4096 x 4096 14.1 and 18.7 us, 256 x 2048 x 8192 20.2 and
 //   32.4, 512 x 8192 x 8192 77 and 89.
 // Returns false where the split does not pay.
-static bool dispatch_splitk(const Args &a, int la, int lb, int dtype, hipStream_t s, const RowColScale &sc,
+static bool dispatch_splitk(const Args &a, int la, int lb, const Wanted &w, hipStream_t s, const RowColScale &sc,
                             hipError_t &e) {
   const int64_t tiles = ceil_div(a.M, 64) * ceil_div(a.N, 64);
-  const bool f32 = dtype == GEMM_E4M3_F32, bf16 = dtype == GEMM_E4M3_BF16;
-  if (tiles <= 256 && a.K >= 1024)
-    e = f32    ? launch_splitk_layout<4, 2, IN_E4M3_AS_BF16, OUT_F32>(a, la, lb, s, sc)
-        : bf16 ? launch_splitk_layout<2, 4, IN_E4M3, OUT_BF16>(a, la, lb, s, sc)
-               : launch_splitk_layout<2, 4, IN_E4M3, OUT_F16>(a, la, lb, s, sc);
-  else if (tiles > 256 && tiles <= 1024 && a.K >= 4096)
-    e = f32    ? launch_splitk_layout<2, 2, IN_E4M3_AS_BF16, OUT_F32>(a, la, lb, s, sc)
-        : bf16 ? launch_splitk_layout<2, 2, IN_E4M3, OUT_BF16>(a, la, lb, s, sc)
-               : launch_splitk_layout<2, 2, IN_E4M3, OUT_F16>(a, la, lb, s, sc);
-  else
-    return false;
+  const bool few = tiles <= 256 && a.K >= 1024, more = tiles > 256 && tiles <= 1024 && a.K >= 4096;
+  if (!few && !more) return false;
+  e = with_types<IN_E4M3>(w, [&](auto in, auto out) {
+    constexpr int IN = decltype(in)::value, OUT = decltype(out)::value;
+    if (more) return launch_splitk_layout<2, 2, IN, OUT>(a, la, lb, s, sc);
+    if constexpr (IN == IN_E4M3)
+      return launch_splitk_layout<2, 4, IN, OUT>(a, la, lb, s, sc);
+    else
+      return launch_splitk_layout<4, 2, IN, OUT>(a, la, lb, s, sc);
+  });
   return true;
 }
 
 // Waves of a workgroup: as many as K has blocks for, up to eight.
-template <int AR, int NT, int OUT>
+template <int AR, int NT, int IN, int OUT>
 static hipError_t launch_rows(const Args &a, hipStream_t stream, RowColScale sc) {
   using T = RowsE4M3<AR, NT>;
   int waves = 1;
@@ -93,18 +111,19 @@ static hipError_t launch_rows(const Args &a, hipStream_t stream, RowColScale sc)
   int tiles_m = (int)ceil_div(a.M, 16 * T::RB);
   const int64_t tiles = tiles_m * ceil_div(a.N, 16 * NT);
   void *params[] = {&A, &B, &C, &M, &N, &K, &lda, &ldb, &ldc, &tiles_m, &sc};
-  return hipLaunchKernel((const void *)lds_gemm_rows_e4m3_kernel<AR, NT, OUT>, dim3((unsigned)tiles),
+  return hipLaunchKernel((const void *)lds_gemm_rows_e4m3_kernel<AR, NT, IN, OUT>, dim3((unsigned)tiles),
                          dim3(64u * waves), params,
                          (size_t)waves * (T::SLICE > 1024 * T::RB * NT ? T::SLICE : 1024 * T::RB * NT), stream);
 }
 
+// From 33 rows on 16-bit outputs take the fp8 MFMA (128 x 4096 x 4096 9.7 and
+// 8.7 us, 192 x 2048 x 8192 14.5 and 12.0); with fewer HBM is the bound and the
+// exact form costs nothing.
 template <int AR, int NT>
-static hipError_t launch_rows_out(const Args &a, int dtype, hipStream_t s, const RowColScale &sc) {
-  switch (dtype) {
-    case GEMM_E4M3_F32: return launch_rows<AR, NT, OUT_F32>(a, s, sc);
-    case GEMM_E4M3_BF16: return launch_rows<AR, NT, OUT_BF16>(a, s, sc);
-    default: return launch_rows<AR, NT, OUT_F16>(a, s, sc);
-  }
+static hipError_t launch_rows_out(const Args &a, const Wanted &w, hipStream_t s, const RowColScale &sc) {
+  return with_types<(AR > 32 ? IN_E4M3 : IN_E4M3_AS_BF16)>(w, [&](auto in, auto out) {
+    return launch_rows<AR, NT, decltype(in)::value, decltype(out)::value>(a, s, sc);
+  });
 }
 
 // Column blocks: two if tiles of one would be more than the 256 CUs (measured
@@ -112,10 +131,10 @@ static hipError_t launch_rows_out(const Args &a, int dtype, hipStream_t s, const
 // 6.0; but 64 x 4096 x 4096 7.9 and 9.6); one where at most 8 rows make the
 // activations' share small (4 x 8192 x 8192: 12.5 us with one, 13.0 with two).
 template <int AR>
-static hipError_t dispatch_rows(const Args &a, int dtype, hipStream_t s, const RowColScale &sc) {
+static hipError_t dispatch_rows(const Args &a, const Wanted &w, hipStream_t s, const RowColScale &sc) {
   if (AR > 8 && ceil_div(a.M, AR < 16 ? 16 : AR) * ceil_div(a.N, 16) > 256)
-    return launch_rows_out<AR, 2>(a, dtype, s, sc);
-  return launch_rows_out<AR, 1>(a, dtype, s, sc);
+    return launch_rows_out<AR, 2>(a, w, s, sc);
+  return launch_rows_out<AR, 1>(a, w, s, sc);
 }
 
 // With both operands K-contiguous the few-rows kernel takes M <= 32, and more
@@ -133,18 +152,18 @@ static bool few_rows(const Args &a, int la, int lb) {
 
 // Otherwise the split-K tiles where they pay, and the shape classes of
 // gemm_run's E4M3 products.
-static hipError_t dispatch_scaled(const Args &a, int la, int lb, int dtype, hipStream_t s, const RowColScale &sc) {
+static hipError_t dispatch_scaled(const Args &a, int la, int lb, const Wanted &w, hipStream_t s, const RowColScale &sc) {
   if (few_rows(a, la, lb)) {
-    if (a.M <= 8) return dispatch_rows<8>(a, dtype, s, sc);
-    if (a.M <= 16) return dispatch_rows<16>(a, dtype, s, sc);
-    if (a.M <= 32) return dispatch_rows<32>(a, dtype, s, sc);
+    if (a.M <= 8) return dispatch_rows<8>(a, w, s, sc);
+    if (a.M <= 16) return dispatch_rows<16>(a, w, s, sc);
+    if (a.M <= 32) return dispatch_rows<32>(a, w, s, sc);
     // tiles of 48 rows where they pad M less than 64 (96 x 4096 x 8192 11.0 and 12.5 us)
-    return ceil_div(a.M, 48) * 48 < ceil_div(a.M, 64) * 64 ? dispatch_rows<48>(a, dtype, s, sc)
-                                                           : dispatch_rows<64>(a, dtype, s, sc);
+    return ceil_div(a.M, 48) * 48 < ceil_div(a.M, 64) * 64 ? dispatch_rows<48>(a, w, s, sc)
+                                                           : dispatch_rows<64>(a, w, s, sc);
   }
-  if (a.M <= 32) return launch_scaled<SkinnyStream8, SKINNY, IN_E4M3_AS_BF16>(a, la, lb, dtype, s, sc);
+  if (a.M <= 32) return launch_scaled<SkinnyStream8, SKINNY, IN_E4M3_AS_BF16>(a, la, lb, w, s, sc);
   hipError_t e;
-  if (dispatch_splitk(a, la, lb, dtype, s, sc, e)) return e;
+  if (dispatch_splitk(a, la, lb, w, s, sc, e)) return e;
   // The 256 x 256 tile also wins with fewer workgroups than CUs where it
   // replaces more than two rounds of 128 x 128 tiles.  bf16 output, ping-pong
   // against 128 x 128: 1100 x 8192 x 8192 79 and 141 us, 2048 x 5000 x 3200 42 and
@@ -152,11 +171,11 @@ static hipError_t dispatch_scaled(const Args &a, int la, int lb, int dtype, hipS
   // 46, 1024 x 8192 x 8192 97 and 89 (fp32 output 86 and 79, 164 and 165).
   const int64_t t128 = ceil_div(a.M, 128) * ceil_div(a.N, 128);
   if (ceil_div(a.M, 256) * ceil_div(a.N, 256) >= 256 || t128 > 512)
-    return launch_scaled<PingPong8, PINGPONG>(a, la, lb, dtype, s, sc);
+    return launch_scaled<PingPong8, PINGPONG>(a, la, lb, w, s, sc);
   if (t128 >= 256)
-    return launch_scaled<DmaMid8, DMA>(a, la, lb, dtype, s, sc);
-  if (small_tile_four_stages(a, 1)) return launch_scaled<DmaSmall8, DMA4>(a, la, lb, dtype, s, sc);
-  return launch_scaled<DmaSmall8, DMA>(a, la, lb, dtype, s, sc);
+    return launch_scaled<DmaMid8, DMA>(a, la, lb, w, s, sc);
+  if (small_tile_four_stages(a, 1)) return launch_scaled<DmaSmall8, DMA4>(a, la, lb, w, s, sc);
+  return launch_scaled<DmaSmall8, DMA>(a, la, lb, w, s, sc);
 }
 
 }  // namespace lsm
@@ -167,6 +186,8 @@ extern "C" int gemm_scaled_run(gemm_handle_t h, const void *A, const void *B, vo
                                hipStream_t stream) {
   using namespace lsm;
   if (!h || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+  const bool exact = dtype >= 0 && (dtype & GEMM_EXACT_SUMS);
+  if (exact) dtype -= GEMM_EXACT_SUMS;
   if (dtype != GEMM_E4M3_F32 && dtype != GEMM_E4M3_BF16 && dtype != GEMM_E4M3_F16) return GEMM_ERR_INVALID_ARG;
   if ((incA != 0 && incA != 1) || (incB != 0 && incB != 1)) return GEMM_ERR_INVALID_ARG;
   const int64_t out_size = dtype == GEMM_E4M3_F32 ? 4 : 2;
@@ -182,7 +203,8 @@ extern "C" int gemm_scaled_run(gemm_handle_t h, const void *A, const void *B, vo
 
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess || dev != h->device) return GEMM_ERR_DEVICE;
-  if (dispatch_scaled(args, layoutA, layoutB, dtype, stream, RowColScale{SA, SB, incA, incB}) != hipSuccess)
+  const Wanted w{dtype == GEMM_E4M3_F32 ? OUT_F32 : dtype == GEMM_E4M3_BF16 ? OUT_BF16 : OUT_F16, exact};
+  if (dispatch_scaled(args, layoutA, layoutB, w, stream, RowColScale{SA, SB, incA, incB}) != hipSuccess)
     return GEMM_ERR_LAUNCH;
   return GEMM_OK;
 }

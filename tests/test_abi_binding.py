@@ -81,3 +81,19 @@ def test_one_build_for_every_python():
     # what the stable ABI's own macros expand to
     assert {n for n in names if n.startswith("_Py")} <= {"_Py_Dealloc", "_Py_NoneStruct"}
     assert "PyType_GetFlags" in names          # PyLong_Check through a call, not through the type's fields
+
+
+E4M3 = (lsm.GEMM_E4M3_F32, lsm.GEMM_E4M3_BF16, lsm.GEMM_E4M3_F16)
+
+
+def test_where_exact_sums_may_be_asked_for():
+    flag = lsm.GEMM_EXACT_SUMS
+    for d in E4M3:
+        assert lsm.gemm_scaled_run(FAKE, **{**SCALED, "dtype": d + flag}) == VALID
+        assert lsm.gemm_scaled_run(FAKE, **{**SCALED, "dtype": d + 2 * flag}) == lsm.GEMM_ERR_INVALID_ARG
+        assert lsm.gemm_scaled_run(FAKE, **{**SCALED, "dtype": d - (1 << 31)}) == lsm.GEMM_ERR_INVALID_ARG
+        assert lsm.gemm_run(FAKE, **{**RUN, "dtype": d + flag}) == lsm.GEMM_ERR_INVALID_ARG
+    for d in (0, 1, 2, 3, 7):
+        assert lsm.gemm_scaled_run(FAKE, **{**SCALED, "dtype": d + flag}) == lsm.GEMM_ERR_INVALID_ARG
+    assert lsm.gemm_w4_run(FAKE, **{**W4, "dtype": W4["dtype"] + flag}) == lsm.GEMM_ERR_INVALID_ARG
+    assert lsm.gemm_rmsnorm_run(FAKE, **{**NORM, "dtype": NORM["dtype"] + flag}) == lsm.GEMM_ERR_INVALID_ARG
