@@ -167,7 +167,8 @@ int gemm_scaled_run(gemm_handle_t h, const void *A, const void *B, void *C,
  *   K            a multiple of 32; K == 0 writes zeros and reads nothing.
  *   group        a power of two, 32 or more; the last group may be cut short
  *                by K, and a group of K or more is one scale for a column.
- *   lda, ldb >= K, lda < 2^24, ldb < 2^25; lds, ldz, ldc >= N and < 2^40.
+ *   lda, ldb >= K, lda < 2^24, ldb < 2^25; lds, ldc >= N, ldz >= N with Z, each
+ *                < 2^40.
  * An entry whose sum over 16 + q and its correction is not finite is summed
  * again term by term, so infinities and NaNs come out as the formula has them.
  *   dtype        GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_F16_F16 or GEMM_F16_F32.

@@ -92,7 +92,7 @@ extern "C" int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const 
 
   const int64_t kMaxDim = (int64_t)1 << 30, kMaxLd = (int64_t)1 << 40;
   if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return GEMM_ERR_UNSUPPORTED;
-  if (lda >= kMaxLd || ldb >= kMaxLd || lds >= kMaxLd || ldz >= kMaxLd || ldc >= kMaxLd)
+  if (lda >= kMaxLd || ldb >= kMaxLd || lds >= kMaxLd || (Z && ldz >= kMaxLd) || ldc >= kMaxLd)
     return GEMM_ERR_UNSUPPORTED;
   // 32-bit offsets inside a tile of 64 rows or columns
   if (K > 0 && (lda >= ((int64_t)1 << 24) || ldb >= ((int64_t)1 << 25))) return GEMM_ERR_UNSUPPORTED;

@@ -97,3 +97,9 @@ def test_where_exact_sums_may_be_asked_for():
         assert lsm.gemm_scaled_run(FAKE, **{**SCALED, "dtype": d + flag}) == lsm.GEMM_ERR_INVALID_ARG
     assert lsm.gemm_w4_run(FAKE, **{**W4, "dtype": W4["dtype"] + flag}) == lsm.GEMM_ERR_INVALID_ARG
     assert lsm.gemm_rmsnorm_run(FAKE, **{**NORM, "dtype": NORM["dtype"] + flag}) == lsm.GEMM_ERR_INVALID_ARG
+
+
+def test_strides_of_absent_operands_do_not_count():
+    assert lsm.gemm_w4_run(FAKE, **{**W4, "Z": 0, "ldz": 1 << 40}) == VALID
+    assert lsm.gemm_w4_run(FAKE, **{**W4, "Z": 0, "ldz": -1}) == VALID
+    assert lsm.gemm_rmsnorm_run(FAKE, **{**NORM, "R": 0, "ldr": 1 << 40, "H": 0, "ldh": -1}) == VALID
