@@ -170,7 +170,8 @@ int gemm_scaled_run(gemm_handle_t h, const void *A, const void *B, void *C,
  *   lda, ldb >= K, lda < 2^24, ldb < 2^25; lds, ldc >= N, ldz >= N with Z, each
  *                < 2^40.
  * An entry whose sum over 16 + q and its correction is not finite is summed
- * again term by term, so infinities and NaNs come out as the formula has them.
+ * again term by term in fp64, so infinities and NaNs come out as the formula has
+ * them, and finite sums of terms beyond fp32 too.
  *   dtype        GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_F16_F16 or GEMM_F16_F32.
  * C is 4-byte (fp32) or 2-byte aligned and overlaps no input. */
 int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const void *S,

@@ -241,7 +241,8 @@ __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsE4M3<AR, NT>::WAVES_PER_
 //  * An infinite activation would turn a (16 + q) - (16 + z) a into a NaN, and
 //    a very large one might overflow there or before it meets a small scale,
 //    where the definition has a finite or infinite value: an entry that is not
-//    finite is therefore summed again term by term.
+//    finite is therefore summed again term by term, in fp64, whose range holds
+//    every product of three factors and every sum of them.
 typedef _Float16 v2f16 __attribute__((ext_vector_type(2)));
 
 template <int IN>
@@ -327,17 +328,17 @@ struct W4Args {
   uint32_t zmask, zadd;               // zero point = (byte & zmask) + zadd
 };
 
-// One entry, summed term by term in the order of k; 32 of them, which share a
-// scale, are loaded at once.
+// One entry, summed term by term in the order of k, in fp64; 32 of them, which
+// share a scale, are loaded at once.  A NaN ends it: the sum stays one.
 template <int IN>
 __device__ __forceinline__ float w4_entry(const W4Args &p, int m, int n) {
   const uint16_t *a = p.A + (int64_t)m * p.lda;
   const uint8_t *b = p.B + (int64_t)n * p.ldb;
-  float v = 0.f;
-  for (int k = 0; k < p.K; k += 32) {
+  double v = 0.;
+  for (int k = 0; k < p.K && !__builtin_isnan(v); k += 32) {
     const int64_t gi = k >> p.gshift;
     const int z = (int)((p.Z[gi * p.ldz + n] & p.zmask) + p.zadd);
-    const float s = to_f32<IN>(p.S[gi * p.lds + n]);
+    const double s = to_f32<IN>(p.S[gi * p.lds + n]);
     const u32x4 q = *(const u32x4 *)(b + k / 2);
     u32x4 x[4];
 #pragma unroll
@@ -347,10 +348,10 @@ __device__ __forceinline__ float w4_entry(const W4Args &p, int m, int n) {
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         const uint32_t pair = x[j][i / 2];
-        v += to_f32<IN>((uint16_t)(pair >> (16 * (i & 1)))) * ((float)((int)((q[j] >> (4 * i)) & 15) - z) * s);
+        v += to_f32<IN>((uint16_t)(pair >> (16 * (i & 1)))) * ((double)((int)((q[j] >> (4 * i)) & 15) - z) * s);
       }
   }
-  return v;
+  return (float)v;
 }
 
 // The dword of lane 16 t + c, for every t, in every lane (c = lane & 15): rows

@@ -56,3 +56,21 @@ def test_norm_whose_squares_overflow(N):
             assert (S[:3] == np.float32(2.0 ** -100) / np.float32(448)).all()
         _, y = R.rmsnorm(x[3:], None, w, 1e-5)
         T.check_norm(1, N, "bf16", out, (None, y, None, Y[3:], S[3:]))
+
+
+@pytest.mark.parametrize("M,N", [(1, 40), (20, 40), (40, 4200)])
+def test_w4_terms_beyond_the_range(M, N):
+    """Entries whose factors or partial sums overflow fp32 where the formula's sum does not: a scale so
+    large that (q - z) s overflows beside activations that are zero or tiny, and large terms that cancel."""
+    K, group = 64, 32
+    q, z, s, a = np.full((N, K), 15), np.full((2, N), 3.0), np.ones((2, N)), np.zeros((M, K))
+    s[0] = 2.0 ** 125                              # 12 * 2^125 is beyond fp32
+    a[:, 1], a[:, 40] = -2.0 ** -60, np.inf
+    got = T.run_w4(a, q, s, z, group, "bf16", "f32")
+    assert (got == np.inf).all()
+
+    s[0], a[:, 1], a[:, 40] = 1.0, 0.0, 0.0
+    z[1], q[:, 33], q[:, 34], q[:, 35] = 8, 13, 3, 9
+    a[:, 33:36] = 2.0 ** 127, 2.0 ** 127, 3.0      # 5 * 2^127 - 5 * 2^127 + 3
+    got = T.run_w4(a, q, s, z, group, "bf16", "f32")
+    assert (got == 3.0).all()
