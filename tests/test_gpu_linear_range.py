@@ -74,3 +74,23 @@ def test_w4_terms_beyond_the_range(M, N):
     a[:, 33:36] = 2.0 ** 127, 2.0 ** 127, 3.0      # 5 * 2^127 - 5 * 2^127 + 3
     got = T.run_w4(a, q, s, z, group, "bf16", "f32")
     assert (got == 3.0).all()
+
+
+@pytest.mark.parametrize("kind,out", sorted(T.W4))
+@pytest.mark.parametrize("M", [1, 16, 20, 48])
+@pytest.mark.parametrize("data", ["biased", "loud"])
+def test_w4_activations_with_a_mean_and_with_outliers(kind, out, M, data):
+    """The header's bound where the zero point's correction cancels most: activations far from zero in
+    the mean, and outliers that meet weights of zero (q = z)."""
+    N, K, group = 272, 4096, 128
+    rng = np.random.default_rng([M, len(data)])
+    a = rng.standard_normal((M, K)) + (2 if data == "biased" else 0)
+    q, z = rng.integers(0, 16, (N, K)), rng.integers(0, 16, (K // group, N)).astype(np.float64)
+    s = R.round_to((0.5 + rng.random(z.shape)) / 64, kind)
+    if data == "loud":
+        for k in range(5, K, 500):
+            a[:, k], q[:, k] = 1e4, z[k // group]
+    a = R.round_to(a, kind)
+    got = T.run_w4(a, q, s, z, group, kind, out)
+    ref, bound = R.w4(a, q, s, z, group)
+    R.assert_within(got, ref, bound + (bound + np.abs(ref)) * R.HALF_STEP[out] + R.SMALLEST[out], "w4 " + data)
