@@ -94,3 +94,25 @@ def test_w4_activations_with_a_mean_and_with_outliers(kind, out, M, data):
     got = T.run_w4(a, q, s, z, group, kind, out)
     ref, bound = R.w4(a, q, s, z, group)
     R.assert_within(got, ref, bound + (bound + np.abs(ref)) * R.HALF_STEP[out] + R.SMALLEST[out], "w4 " + data)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N", [(1, 40), (5, 40), (5, 4100), (20, 40), (20, 4100), (20, 8200), (48, 40), (48, 4100),
+                                 (48, 8200)])
+def test_w4_zero_points_of_every_byte(kind, group, M, N):
+    """Zero points from 0 to 255, in one, two and four blocks of columns."""
+    K = 288
+    a, q, s, _ = T.w4_inputs(M, N, K, group, kind, True, "int")
+    z = np.random.default_rng([M, N, group]).integers(0, 256, s.shape).astype(np.float64)
+    # |a| <= 2, 16 + q <= 31, 16 + z <= 271 and s >= 1/4: sums below 2^24 in units of 1/4
+    assert 2 * (31 + 271) * 4 * K < 1 << 24
+    got = T.run_w4(a, q, s, z, group, kind, "f32")
+    assert np.array_equal(got, R.w4(a, q, s, z, group)[0])
+
+
+@pytest.mark.parametrize("M", [1, 3, 8, 9, 16, 17, 32, 33, 48, 49, 64])
+@pytest.mark.parametrize("N,K", [(33, 48), (200, 1040), (4099, 272), (8208, 144)])
+def test_scaled_few_rows_fp16(M, N, K):
+    for dist in ("int", "real"):
+        T.check_scaled(M, N, K, T.KC, T.KC, "f16", dist, extra=N % 3)
