@@ -53,6 +53,11 @@ def library_path() -> str:
     return os.path.join(_HERE, _LIB_NAME)
 
 
+# The linear layer's entry points: pointers, 64-bit sizes and what follows them before the stream.
+_LAYER = (("gemm_scaled_run", 5, 6, [ctypes.c_int] * 5), ("gemm_w4_run", 5, 9, [ctypes.c_int]),
+          ("gemm_rmsnorm_run", 6, 6, [ctypes.c_float, ctypes.c_int]))
+
+
 def _open(path):
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: build it with lds_staged_matrix_amd/build.py "
@@ -67,6 +72,10 @@ def _open(path):
     lib.gemm_destroy.restype = i32
     lib.gemm_status_str.argtypes = [i32]
     lib.gemm_status_str.restype = ctypes.c_char_p
+    for name, pointers, sizes, tail in _LAYER:
+        if hasattr(lib, name):          # not in the A/B builds of gemm_run alone
+            fn = getattr(lib, name)
+            fn.argtypes, fn.restype = [vp] * (1 + pointers) + [i64] * sizes + tail + [vp], i32
     return lib
 
 
@@ -166,7 +175,8 @@ def gemm_status_str(status: int) -> str:
 class Library:
     """gemm_create, gemm_run, gemm_destroy and gemm_status_str bound to one
     specific build of the library (the default build, or an A/B build from
-    ablation_library(); an A/B build holds these four and nothing else)."""
+    ablation_library()); the linear layer's entry points where the build has
+    them (the default build and "poison")."""
 
     def __init__(self, path):
         self.path = path
@@ -184,6 +194,24 @@ class Library:
         return self._lib.gemm_run(h, _ptr(A), _ptr(B), _ptr(C),
                                   *_sizes(M, N, K, lda, ldb, ldc, layoutA, layoutB, dtype),
                                   _stream(stream))
+
+    def _layer(self, name, h, args, stream):
+        _, np, nw, tail = next(e for e in _LAYER if e[0] == name)
+        p, w, t = args[:np], args[np:np + nw], args[np + nw:]
+        return getattr(self._lib, name)(h, *map(_ptr, p), *(_int(v, 64, name) for v in w),
+                                        *(v if c is ctypes.c_float else _int(v, 32, name) for v, c in zip(t, tail)),
+                                        _stream(stream))
+
+    def gemm_scaled_run(self, h, A, B, C, SA, SB, M, N, K, lda, ldb, ldc, incA, incB, layoutA, layoutB, dtype,
+                        stream=None) -> int:
+        return self._layer("gemm_scaled_run", h, (A, B, C, SA, SB, M, N, K, lda, ldb, ldc, incA, incB, layoutA,
+                                                  layoutB, dtype), stream)
+
+    def gemm_w4_run(self, h, A, B, S, Z, C, M, N, K, group, lda, ldb, lds, ldz, ldc, dtype, stream=None) -> int:
+        return self._layer("gemm_w4_run", h, (A, B, S, Z, C, M, N, K, group, lda, ldb, lds, ldz, ldc, dtype), stream)
+
+    def gemm_rmsnorm_run(self, h, X, R, W, H, Y, S, M, N, ldx, ldr, ldh, ldy, eps, dtype, stream=None) -> int:
+        return self._layer("gemm_rmsnorm_run", h, (X, R, W, H, Y, S, M, N, ldx, ldr, ldh, ldy, eps, dtype), stream)
 
     def gemm_destroy(self, h) -> int:
         return self._lib.gemm_destroy(h)

@@ -23,7 +23,9 @@ LIB = os.path.join(PKG, "liblds_gemm.so")
 BINDING = os.path.join(PKG, "_binding.so")
 ABLATION_DIR = os.path.join(PKG, "ablation")
 SOURCES = ["gemm_api.hip", "gemm_scaled.hip", "gemm_w4.hip", "gemm_norm.hip"]
-VARIANT_SOURCES = ["gemm_api.hip"]     # the A/B builds change gemm_run's kernels
+# Most A/B builds change gemm_run's kernels only; these change every kernel that uses LDS.
+VARIANT_SOURCES = ["gemm_api.hip"]
+WHOLE_VARIANTS = ("poison",)
 OBJ_DIR = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC",
@@ -81,19 +83,25 @@ def build(verbose: bool = False, extra_flags=(), variant: str = None) -> str:
     if variant is not None:
         os.makedirs(ABLATION_DIR, exist_ok=True)
         out = variant_path(variant)
+        if variant in WHOLE_VARIANTS:
+            return _build_library(out, "_" + variant, verbose, [*VARIANTS[variant], *extra_flags])
         cmd = [HIPCC, *FLAGS, *VARIANTS[variant], *extra_flags, "-shared",
                *[os.path.join(CSRC, s) for s in VARIANT_SOURCES], "-o", out + ".tmp"]
         return _run(cmd, out, verbose)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
-        objs = list(pool.map(lambda s: build_object(s, verbose, extra_flags), SOURCES))
     build_binding(verbose)
-    return _run([HIPCC, *FLAGS, "-shared", *objs, "-o", LIB + ".tmp"], LIB, verbose)
+    return _build_library(LIB, "", verbose, extra_flags)
 
 
-def build_object(source: str, verbose: bool = False, extra_flags=()) -> str:
+def _build_library(out, suffix, verbose, extra_flags):
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+        objs = list(pool.map(lambda s: build_object(s, verbose, extra_flags, suffix), SOURCES))
+    return _run([HIPCC, *FLAGS, "-shared", *objs, "-o", out + ".tmp"], out, verbose)
+
+
+def build_object(source: str, verbose: bool = False, extra_flags=(), suffix: str = "") -> str:
     """One translation unit of the library."""
     os.makedirs(OBJ_DIR, exist_ok=True)
-    out = os.path.join(OBJ_DIR, os.path.splitext(source)[0] + ".o")
+    out = os.path.join(OBJ_DIR, os.path.splitext(source)[0] + suffix + ".o")
     cmd = [HIPCC, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, source), "-o", out + ".tmp"]
     return _run(cmd, out, verbose)
 

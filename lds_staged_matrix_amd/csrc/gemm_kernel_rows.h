@@ -43,6 +43,15 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// Poison build: a wave's slice, before the writes of each block.
+template <int BYTES>
+__device__ __forceinline__ void poison_slice(char *slice, int lane) {
+  if constexpr (LSM_LDS_POISON) {
+    lds_poison(slice, BYTES, lane, 64);
+    wave_lds_order();
+  }
+}
+
 // 16 bytes at base + voff + soff: voff one register a lane, constant over the K
 // loop, soff uniform.  (As a flat address the compiler keeps base + voff in two
 // registers and adds to them in every round.)  The record count is no bound
@@ -70,6 +79,11 @@ constexpr int rows_slice_bytes(int arows, int a_es, int bcols, int b_bits) {
   return arows * kRowsBlockK * a_es + bcols * kRowsBlockK * b_bits / 8;
 }
 
+// LDS bytes of a workgroup: the waves' slices, whose place the partial sums take.
+constexpr int rows_lds_bytes(int waves, int slice, int blocks) {
+  return waves * (slice > 1024 * blocks ? slice : 1024 * blocks);
+}
+
 // The workgroup's partial sums, added in wave order through `red` (waves * RB
 // * NT KiB of LDS); `store(m, n, v)` takes each entry of the 16 RB x 16 NT
 // tile, rows and columns counted from the tile's.
@@ -77,6 +91,10 @@ template <int RB, int NT, class Store>
 __device__ __forceinline__ void reduce_rows(const v4f32 (&acc)[RB][NT], float *red, int waves, int wave,
                                             int lane, Store store) {
   constexpr int TILE = RB * NT * 256;
+  if constexpr (LSM_LDS_POISON) {   // poison build: the sums' region, before its writes
+    lds_poison((char *)red, waves * TILE * 4, threadIdx.x, blockDim.x);
+    __syncthreads();
+  }
 #pragma unroll
   for (int i = 0; i < RB; i++)
 #pragma unroll
@@ -171,6 +189,7 @@ __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsE4M3<AR, NT>::WAVES_PER_
   // The products of the loaded block; next() issues the next one's loads.
   auto block = [&](auto next) {
     wave_lds_order();
+    poison_slice<T::SLICE>(slice, lane);
 #pragma unroll
     for (int i = 0; i < LB; i++) *(u32x4 *)(slice + kc_chunk_offset(8 * i + lrow, lchunk, ROW)) = b[i];
 #pragma unroll
@@ -461,6 +480,7 @@ __global__ __launch_bounds__((64 * kRowsMaxWaves), (RowsW4<AR, NT>::WAVES_PER_SI
   auto block = [&](int left, auto next) {
     if constexpr (AR >= 16) __builtin_amdgcn_s_setprio(0);
     wave_lds_order();
+    poison_slice<T::SLICE>(slice, lane);
 #pragma unroll
     for (int t = 0; t < NT; t++)
       *(u32x4 *)(slice + kc_chunk_offset(16 * t + (lane >> 2), lane & 3, BROW)) = b[t];

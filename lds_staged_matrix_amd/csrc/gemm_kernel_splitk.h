@@ -37,6 +37,10 @@ __global__ __launch_bounds__(KS * T::NT, KS / 2) void lds_gemm_splitk_kernel(
   static_assert((NS == 2 || NS == 4) && KS * NS * STAGE <= 160 * 1024, "stages");
   __shared__ __attribute__((aligned(1024))) char smem[KS * NS * STAGE];
 
+  if constexpr (LSM_LDS_POISON) {   // poison build: all of LDS, before any load or write
+    lds_poison(smem, KS * NS * STAGE, threadIdx.x, blockDim.x);
+    __syncthreads();
+  }
   const int lane = threadIdx.x & 63;
   const int gtid = threadIdx.x & (T::NT - 1);            // thread in its group
   const int wave = __builtin_amdgcn_readfirstlane(gtid >> 6);
@@ -124,6 +128,10 @@ __global__ __launch_bounds__(KS * T::NT, KS / 2) void lds_gemm_splitk_kernel(
   // rows exchanged: the two rows that one write of an accumulator register
   // covers are four apart and land in different banks.
   __syncthreads();                       // every wave is past its last LDS read
+  if constexpr (LSM_LDS_POISON) {   // poison build: the sums' region, before its writes
+    lds_poison(smem, KS * TILE_BYTES, threadIdx.x, blockDim.x);
+    __syncthreads();
+  }
   auto at = [](int row, int col) { return row * T::BN + (col ^ (((row >> 2) & 1) << 5)); };
   float *red = (float *)smem;
   using L = AccLayout<32>;

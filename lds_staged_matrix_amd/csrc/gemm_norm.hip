@@ -86,6 +86,10 @@ __device__ __forceinline__ void row_sum_max(float &sum, uint32_t &top, int waves
   wave_sum_max(sum, top);
   __shared__ float s_sum[16];
   __shared__ uint32_t s_top[16];
+  if constexpr (LSM_LDS_POISON) {   // poison build: before the writes
+    if (threadIdx.x < 16) s_sum[threadIdx.x] = __builtin_nanf(""), s_top[threadIdx.x] = ~0u;
+    __syncthreads();
+  }
   if ((threadIdx.x & 63) == 0) {
     s_sum[threadIdx.x >> 6] = sum;
     s_top[threadIdx.x >> 6] = top;

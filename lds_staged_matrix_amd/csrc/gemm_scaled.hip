@@ -113,7 +113,7 @@ static hipError_t launch_rows(const Args &a, hipStream_t stream, RowColScale sc)
   void *params[] = {&A, &B, &C, &M, &N, &K, &lda, &ldb, &ldc, &tiles_m, &sc};
   return hipLaunchKernel((const void *)lds_gemm_rows_e4m3_kernel<AR, NT, IN, OUT>, dim3((unsigned)tiles),
                          dim3(64u * waves), params,
-                         (size_t)waves * (T::SLICE > 1024 * T::RB * NT ? T::SLICE : 1024 * T::RB * NT), stream);
+                         (size_t)rows_lds_bytes(waves, T::SLICE, T::RB * NT), stream);
 }
 
 // From 33 rows on 16-bit outputs take the fp8 MFMA (128 x 4096 x 4096 9.7 and

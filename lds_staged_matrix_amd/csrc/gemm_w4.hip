@@ -47,7 +47,7 @@ static hipError_t launch_w4(const W4Args &p, int waves, hipStream_t stream) {
   const int64_t tiles = a.tiles_m * ceil_div(p.N, 16 * NT);
   void *params[] = {&a};
   return hipLaunchKernel((const void *)lds_gemm_w4_kernel<IN, AR, NT, GS>, dim3((unsigned)tiles), dim3(64u * waves),
-                         params, (size_t)waves * (T::SLICE > 1024 * T::RB * NT ? T::SLICE : 1024 * T::RB * NT), stream);
+                         params, (size_t)rows_lds_bytes(waves, T::SLICE, T::RB * NT), stream);
 }
 
 template <int IN, int AR, int NT>
