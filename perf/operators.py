@@ -164,8 +164,9 @@ def _lib():
 
 
 def _stream():
-    """The stream that the inputs were made on and the outputs are read on."""
-    return torch.cuda.current_stream()
+    """The stream that the inputs were made on and the outputs are read on, by its handle alone:
+    torch.cuda.current_stream() would make a Stream object of it first, in 2.7 us."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(lsm, status, what):
