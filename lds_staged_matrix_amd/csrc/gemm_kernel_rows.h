@@ -66,9 +66,9 @@ __device__ __forceinline__ u32x4 rows_load(__amdgpu_buffer_rsrc_t rs, uint32_t v
 // Where in K a workgroup starts, in blocks of `full`: each XCD at an eighth of
 // its own.  Workgroups that start together everywhere ask for the same
 // kilobyte of rows that lie a power of two apart, which a part of the HBM
-// channels holds: 1 x 16384 x 8192 E4M3 took 31.4 us, with the eighths 25.0
-// (5.4 TB/s); 4 bits, 1 x 28672 x 8192, 31.4 and 28.2 us.  Inside an XCD all start
-// together, so that the activations they share stay in its L2 (a start of
+// channels holds: 1 x 16384 x 8192 E4M3 took 30.0 us, with the eighths 23.2
+// (5.8 TB/s), 32 rows of it 35.2 and 27.2; 4 bits, 1 x 28672 x 8192, 30.0 and 26.9
+// (but 48 x 8192 x 8192 19.7 and 20.3).  Inside an XCD all start together, so that the activations they share stay in its L2 (a start of
 // each tile's own took 16.4 instead of 11.8 us for 1 x 8192 x 8192 E4M3).
 __device__ __forceinline__ int rows_start(int full) {
   return (int)((uint32_t)(blockIdx.x & 7) * (uint32_t)full >> 3);

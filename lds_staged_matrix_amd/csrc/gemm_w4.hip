@@ -11,8 +11,7 @@ namespace lsm {
 
 // Rows of a tile, of which so many are loaded: from 17 on 32 or 48, whichever
 // pads M less (128 x 8192 x 8192 39.4 us with 32 and 50.6 with 48; 192 rows, a tie,
-// 57.5 and 52.3; tiles of 64 rows, whose registers hold two column blocks at
-// most, took 42.8 and 62.6).
+// 57.5 and 52.3).
 static int w4_rows(int64_t M) {
   if (M <= 16) return M <= 4 ? 4 : 16;
   return ceil_div(M, 48) * 48 <= ceil_div(M, 32) * 32 ? 48 : 32;
@@ -94,7 +93,7 @@ extern "C" int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const 
   if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return GEMM_ERR_UNSUPPORTED;
   if (lda >= kMaxLd || ldb >= kMaxLd || lds >= kMaxLd || (Z && ldz >= kMaxLd) || ldc >= kMaxLd)
     return GEMM_ERR_UNSUPPORTED;
-  // 32-bit offsets inside a tile of 64 rows or columns
+  // 32-bit offsets inside a tile of 48 rows and 64 columns
   if (K > 0 && (lda >= ((int64_t)1 << 24) || ldb >= ((int64_t)1 << 25))) return GEMM_ERR_UNSUPPORTED;
   // groups of a power of two of at least 32, and whole 32s of K
   if (group < 32 || (group & (group - 1)) || group > kMaxDim || K % 32) return GEMM_ERR_UNSUPPORTED;
