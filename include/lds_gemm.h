@@ -158,10 +158,10 @@ int gemm_scaled_run(gemm_handle_t h, const void *A, const void *B, void *C,
  * group's sum, sum A (16 + q) - (16 + Z) sum A, or, for fp16 of more than 16 rows,
  * off each weight; so before the rounding an entry is within
  *     2^-23 (min(group, K) + K/group + 21) sum_k |A S| (47 + Z)
- * of the formula, and on ordinary data, also with activations far from zero in
- * the mean, within 3e-7 of itself.  Meant for few rows (M <= 48: the
- * weights are read once); any M is computed, the weights being read again for
- * every 32 or 48 rows.
+ * of the formula; on ordinary data, also with activations far from zero in the
+ * mean, the relative error (2-norm) is 3e-7 at most.  Meant for few rows (M <= 48:
+ * the weights are read once); any M is computed, the weights being read again
+ * for every 32 or 48 rows.
  *   A            bf16/fp16, K-contiguous, 16-byte aligned; lda a multiple of 8.
  *   B            q(k,n) = bits 4*(k&1) .. 4*(k&1)+3 of byte (n*ldb + k)/2: two
  *                weights a byte, K-contiguous, even k in the low half.  16-byte
@@ -195,9 +195,9 @@ int gemm_w4_run(gemm_handle_t h, const void *A, const void *B, const void *S,
  * so that S and Y are the SA and A of gemm_scaled_run.  All arithmetic is
  * fp32, the squares included (rows whose squares' sum overflows there give
  * zeros; with eps == 0, rows whose squares all vanish there give NaN and
- * infinities), and y is computed from h before it is rounded.  A NaN in a row makes
- * all of its y NaN; an infinity is NaN at its place and makes the others zero;
- * with E4M3 output either one makes the row and S[m] NaN.
+ * infinities), and y is computed from h before it is rounded.  A NaN in a row
+ * makes all of its y NaN; an infinity is NaN at its place and makes the others
+ * zero; with E4M3 output either one makes the row and S[m] NaN.
  *   X, R, W, H   elements of the input type, 2-byte aligned; R and H may be
  *                NULL (no residual; h not wanted).
  *   Y            input type (2-byte aligned) or E4M3; S is used for E4M3 only.
