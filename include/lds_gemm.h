@@ -82,6 +82,14 @@ enum gemm_dtype {
  * output too, at up to twice the time (fp32 output always has them). */
 enum { GEMM_EXACT_SUMS = 0x100 };
 
+/* The 16- or 32-bit type beside MXFP4: of the matrix that is quantised, of the
+ * values that come back, of a product's C. */
+enum gemm_mxfp4_dtype {
+    GEMM_MXFP4_BF16 = 0,
+    GEMM_MXFP4_F16 = 1,
+    GEMM_MXFP4_F32 = 2
+};
+
 /* Element types of gemm_rmsnorm_run, named input_output. */
 enum gemm_norm_dtype {
     GEMM_NORM_BF16_BF16 = 0,
@@ -210,6 +218,111 @@ int gemm_rmsnorm_run(gemm_handle_t h, const void *X, const void *R, const void *
                      int64_t M, int64_t N,
                      int64_t ldx, int64_t ldr, int64_t ldh, int64_t ldy,
                      float eps, int dtype, hipStream_t stream);
+
+/* Enqueue the conversion of the M x K matrix X to MXFP4 on `stream`.
+ *
+ * MXFP4 (OCP Microscaling Formats 1.0): 4-bit E2M1 elements (0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and a sign) and one E8M0 scale, 2^(S - 127), for every block of 32
+ * consecutive k.  An MXFP4 matrix of M rows is two arrays:
+ *     Q    q(m,k) = bits 4*(k&1) .. 4*(k&1)+3 of byte (m*ldq + k)/2: two elements
+ *          a byte, even k in the low half;
+ *     S    S[(k/32)*lds + m]: a row of M scales for each 32 k.
+ * For each block, with the largest |x| in it,
+ *     S = 255 (NaN) and zero elements if the block holds an infinity or a NaN;
+ *     S = max(floor(log2(max|x|)) - 2 + 127, 0), or 0 for a block of zeros, and
+ *     q = x / 2^(S - 127), rounded to nearest even, sizes beyond 6 to 6.
+ *   X            bf16, fp16 or fp32 elements (dtype), aligned to their size;
+ *                layoutX GEMM_K_CONTIG: x(m,k) = X[m*ldx + k], ldx >= K;
+ *                GEMM_MN_CONTIG: x(m,k) = X[k*ldx + m], ldx >= M.
+ *   Q            16-byte aligned; ldq >= K counts elements, a multiple of 32.
+ *   S            16-byte aligned bytes; lds >= M, a multiple of 16.
+ *   M, K         sizes, K a multiple of 32; M == 0 or K == 0 is a no-op.
+ * Of Q and S only what stands for the M x K elements is written.  X, Q and S do
+ * not overlap. */
+int gemm_mxfp4_quantize_run(gemm_handle_t h, const void *X, void *Q, void *S,
+                            int64_t M, int64_t K, int64_t ldx, int64_t ldq, int64_t lds,
+                            int layoutX, int dtype, hipStream_t stream);
+
+/* Enqueue the values of an MXFP4 matrix on `stream`:
+ *     Y[m*ldy + k] = q(m,k) * 2^(S[(k/32)*lds + m] - 127)
+ * rounded to dtype's type, to nearest even (bf16 and fp32 hold every such value
+ * but those beyond their range); a NaN scale makes its block NaN.  Arguments as
+ * for gemm_mxfp4_quantize_run, with ldy >= K; Y does not overlap Q or S. */
+int gemm_mxfp4_dequantize_run(gemm_handle_t h, const void *Q, const void *S, void *Y,
+                              int64_t M, int64_t K, int64_t ldq, int64_t lds, int64_t ldy,
+                              int dtype, hipStream_t stream);
+
+/* Enqueue the product of two MXFP4 matrices on `stream`, B being N x K:
+ *     C[m][n] = round( sum_k qa(m,k) 2^(SA[(k/32)*ldsa + m] - 127)
+ *                          * qb(n,k) 2^(SB[(k/32)*ldsb + n] - 127) )
+ * Products are exact and summed in fp32 by the matrix cores, with one rounding to
+ * C's type: before it an entry is within 2^-22 (K/128 + 8) sum_k |a b| of the
+ * formula.  A NaN scale makes its row or column NaN; sums beyond fp32 are
+ * infinite.
+ *   A, SA, B, SB MXFP4 matrices as gemm_mxfp4_quantize_run writes them.  The bytes
+ *                between M (N) and the next multiple of 16 in a row of scales
+ *                belong to the array (its last row too), whatever they hold.
+ *   lda, ldb     >= K, multiples of 32, < 2^23;  ldsa >= M, ldsb >= N, multiples
+ *                of 16, < 2^27.
+ *   C            of dtype's type, aligned to its size, ldc >= N, overlaps no input.
+ * K == 0 writes zeros; M == 0 or N == 0 is a no-op. */
+int gemm_mxfp4_run(gemm_handle_t h, const void *A, const void *B, void *C,
+                   const void *SA, const void *SB,
+                   int64_t M, int64_t N, int64_t K,
+                   int64_t lda, int64_t ldb, int64_t ldc, int64_t ldsa, int64_t ldsb,
+                   int dtype, hipStream_t stream);
+
+/* Grouped products: T rows, sorted by group (expert), of which group g has rows
+ * ends[g-1] .. ends[g]-1, the first group from row 0.  `ends` are G int32 on the
+ * device, read when the work runs; nothing about the groups is known to the host.
+ * An end below the ends before it counts as the largest of them, a negative one
+ * as 0 and one beyond T as T, so that groups are disjoint and inside the T rows whatever
+ * `ends` holds.  Groups may be empty, and rows behind the last group belong to
+ * none. */
+
+/* Enqueue, on `stream`, each group's rows times the group's own matrix:
+ *     C[t*ldc + n] = round( sum_k A[t*lda + k] * b(g,k,n) )   for t in group g
+ *     layoutB == GEMM_K_CONTIG : b(g,k,n) = B[g*strideb + n*ldb + k]
+ *     layoutB == GEMM_MN_CONTIG: b(g,k,n) = B[g*strideb + k*ldb + n]
+ * Rows of C that belong to no group are left as they were.  With dC in A's place
+ * and B's other layout (N and K exchanged) it is the gradient of the rows.
+ *   A, B         bf16 or fp16, 16-byte aligned; lda >= K, ldb >= K (or N),
+ *                lda, ldb < 2^21; lda, ldb and strideb >= 0 multiples of 8
+ *                (0: one matrix for all groups).
+ *   K            a multiple of 8, and N too where B is MN-contiguous.  K == 0
+ *                writes zeros.  G == 0, T == 0 or N == 0 is a no-op.
+ *   C            aligned to its elements, ldc >= N, overlaps no input.
+ *   dtype        GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_F16_F16 or GEMM_F16_F32. */
+int gemm_grouped_run(gemm_handle_t h, const void *A, const void *B, void *C,
+                     const int32_t *ends, int64_t G, int64_t T, int64_t N, int64_t K,
+                     int64_t lda, int64_t ldb, int64_t strideb, int64_t ldc,
+                     int layoutB, int dtype, hipStream_t stream);
+
+/* Enqueue, on `stream`, the gradient of the groups' matrices:
+ *     C[g*stridec + m*ldc + n] = round( sum over t in group g of
+ *                                       A[t*lda + m] * B[t*ldb + n] )
+ * An empty group's matrix is all zeros.  A and B are the forward's rows and the
+ * gradient of its C, in the order that gives C the layout wanted.
+ *   A, B         bf16 or fp16, 16-byte aligned; lda >= M, ldb >= N, multiples of
+ *                8, < 2^21; M and N multiples of 8.
+ *   C            aligned to its elements, ldc >= N, stridec >= (M-1)*ldc + N;
+ *                overlaps no input.  G == 0, M == 0 or N == 0 is a no-op.
+ *   dtype        as for gemm_grouped_run. */
+int gemm_grouped_wgrad_run(gemm_handle_t h, const void *A, const void *B, void *C,
+                           const int32_t *ends, int64_t G, int64_t T, int64_t M, int64_t N,
+                           int64_t lda, int64_t ldb, int64_t ldc, int64_t stridec,
+                           int dtype, hipStream_t stream);
+
+/* Enqueue, on `stream`, each group's MXFP4 rows times the group's own MXFP4
+ * matrix of N x K: gemm_grouped_run's groups, gemm_mxfp4_run's operands and sums.
+ * Group g's elements stand at element g*strideb of B (a multiple of 32) and its
+ * scales at byte g*stridesb of SB (a multiple of 16). */
+int gemm_grouped_mxfp4_run(gemm_handle_t h, const void *A, const void *B, void *C,
+                           const void *SA, const void *SB, const int32_t *ends,
+                           int64_t G, int64_t T, int64_t N, int64_t K,
+                           int64_t lda, int64_t ldb, int64_t strideb, int64_t ldc,
+                           int64_t ldsa, int64_t ldsb, int64_t stridesb,
+                           int dtype, hipStream_t stream);
 
 /* Release a handle.  NULL is accepted and returns GEMM_OK. */
 int gemm_destroy(gemm_handle_t h);

@@ -9,7 +9,10 @@ Names mirror the C ABI: gemm_create, gemm_run, gemm_destroy, gemm_status_str,
 and the operators of a quantised linear layer: gemm_rmsnorm_run (norm with the
 residual's addition, 16-bit or scaled E4M3 output), gemm_scaled_run (E4M3
 product with row and column scales) and gemm_w4_run (few rows times 4-bit
-weights).
+weights); MXFP4: gemm_mxfp4_quantize_run, gemm_mxfp4_dequantize_run and
+gemm_mxfp4_run (the product); and products by group of rows (expert):
+gemm_grouped_run, gemm_grouped_wgrad_run (the matrices' gradient) and
+gemm_grouped_mxfp4_run.
 Pointers may be passed as integers or as objects with a ``data_ptr()`` method
 (torch tensors); streams as integers, objects with a ``cuda_stream``
 attribute (torch streams) or None for the null stream.
@@ -21,10 +24,13 @@ __all__ = [
     "GEMM_K_CONTIG", "GEMM_MN_CONTIG",
     "GEMM_BF16_F32", "GEMM_BF16_BF16", "GEMM_F16_F16", "GEMM_F16_F32", "GEMM_E4M3_F32",
     "GEMM_E4M3_BF16", "GEMM_E4M3_F16", "GEMM_EXACT_SUMS",
+    "GEMM_MXFP4_BF16", "GEMM_MXFP4_F16", "GEMM_MXFP4_F32",
     "GEMM_NORM_BF16_BF16", "GEMM_NORM_BF16_E4M3", "GEMM_NORM_F16_F16", "GEMM_NORM_F16_E4M3",
     "GEMM_OK", "GEMM_ERR_INVALID_ARG", "GEMM_ERR_UNSUPPORTED", "GEMM_ERR_DEVICE",
     "GEMM_ERR_LAUNCH", "GemmError", "library_path", "load_library", "gemm_create",
-    "gemm_run", "gemm_scaled_run", "gemm_w4_run", "gemm_rmsnorm_run", "gemm_destroy",
+    "gemm_run", "gemm_scaled_run", "gemm_w4_run", "gemm_rmsnorm_run", "gemm_mxfp4_quantize_run",
+    "gemm_mxfp4_dequantize_run", "gemm_mxfp4_run", "gemm_grouped_run", "gemm_grouped_wgrad_run",
+    "gemm_grouped_mxfp4_run", "gemm_destroy",
     "gemm_status_str", "EXPORTED_SYMBOLS", "Library", "ablation_library",
 ]
 
@@ -33,9 +39,13 @@ GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_F16_F16, GEMM_F16_F32 = 0, 1, 2, 3
 GEMM_E4M3_F32, GEMM_E4M3_BF16, GEMM_E4M3_F16 = 4, 5, 6
 GEMM_EXACT_SUMS = 0x100     # added to gemm_scaled_run's dtype
 GEMM_NORM_BF16_BF16, GEMM_NORM_BF16_E4M3, GEMM_NORM_F16_F16, GEMM_NORM_F16_E4M3 = range(4)
+GEMM_MXFP4_BF16, GEMM_MXFP4_F16, GEMM_MXFP4_F32 = range(3)
 GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED, GEMM_ERR_DEVICE, GEMM_ERR_LAUNCH = range(5)
-EXPORTED_SYMBOLS = ("gemm_create", "gemm_run", "gemm_scaled_run", "gemm_w4_run", "gemm_rmsnorm_run",
-                    "gemm_destroy", "gemm_status_str")
+# The entry points that enqueue work, in the order that _binding.bind takes them.
+_RUNS = ("gemm_run", "gemm_scaled_run", "gemm_w4_run", "gemm_rmsnorm_run", "gemm_mxfp4_quantize_run",
+         "gemm_mxfp4_dequantize_run", "gemm_mxfp4_run", "gemm_grouped_run", "gemm_grouped_wgrad_run",
+         "gemm_grouped_mxfp4_run")
+EXPORTED_SYMBOLS = ("gemm_create", *_RUNS, "gemm_destroy", "gemm_status_str")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "liblds_gemm.so"
@@ -53,9 +63,12 @@ def library_path() -> str:
     return os.path.join(_HERE, _LIB_NAME)
 
 
-# The linear layer's entry points: pointers, 64-bit sizes and what follows them before the stream.
+# The other entry points: pointers, 64-bit sizes and what follows them before the stream.
 _LAYER = (("gemm_scaled_run", 5, 6, [ctypes.c_int] * 5), ("gemm_w4_run", 5, 9, [ctypes.c_int]),
-          ("gemm_rmsnorm_run", 6, 6, [ctypes.c_float, ctypes.c_int]))
+          ("gemm_rmsnorm_run", 6, 6, [ctypes.c_float, ctypes.c_int]),
+          ("gemm_mxfp4_quantize_run", 3, 5, [ctypes.c_int] * 2), ("gemm_mxfp4_dequantize_run", 3, 5, [ctypes.c_int]),
+          ("gemm_mxfp4_run", 5, 8, [ctypes.c_int]), ("gemm_grouped_run", 4, 8, [ctypes.c_int] * 2),
+          ("gemm_grouped_wgrad_run", 4, 8, [ctypes.c_int]), ("gemm_grouped_mxfp4_run", 6, 11, [ctypes.c_int]))
 
 
 def _open(path):
@@ -95,8 +108,7 @@ def _bind():
         raise RuntimeError(f"_binding.so is missing from {_HERE}: build it with lds_staged_matrix_amd/build.py "
                            "(or __graft_entry__.build()); there is no fallback path")
     from . import _binding
-    _binding.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-                    for name in ("gemm_run", "gemm_scaled_run", "gemm_w4_run", "gemm_rmsnorm_run")))
+    _binding.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _RUNS))
     _native = _binding
     return _native
 
@@ -164,6 +176,38 @@ def gemm_rmsnorm_run(h, X, R, W, H, Y, S, M, N, ldx, ldr, ldh, ldy, eps, dtype, 
     return (_native or _bind()).rmsnorm(h, X, R, W, H, Y, S, M, N, ldx, ldr, ldh, ldy, eps, dtype, stream)
 
 
+def gemm_mxfp4_quantize_run(h, X, Q, S, M, K, ldx, ldq, lds, layoutX, dtype, stream=None) -> int:
+    """Enqueue the conversion of X to MXFP4; returns the gemm_status code."""
+    return (_native or _bind()).mxfp4_quantize(h, X, Q, S, M, K, ldx, ldq, lds, layoutX, dtype, stream)
+
+
+def gemm_mxfp4_dequantize_run(h, Q, S, Y, M, K, ldq, lds, ldy, dtype, stream=None) -> int:
+    """Enqueue the values of an MXFP4 matrix; returns the gemm_status code."""
+    return (_native or _bind()).mxfp4_dequantize(h, Q, S, Y, M, K, ldq, lds, ldy, dtype, stream)
+
+
+def gemm_mxfp4_run(h, A, B, C, SA, SB, M, N, K, lda, ldb, ldc, ldsa, ldsb, dtype, stream=None) -> int:
+    """Enqueue the product of two MXFP4 matrices; returns the gemm_status code."""
+    return (_native or _bind()).mxfp4(h, A, B, C, SA, SB, M, N, K, lda, ldb, ldc, ldsa, ldsb, dtype, stream)
+
+
+def gemm_grouped_run(h, A, B, C, ends, G, T, N, K, lda, ldb, strideb, ldc, layoutB, dtype, stream=None) -> int:
+    """Enqueue each group's rows times the group's matrix; returns the gemm_status code."""
+    return (_native or _bind()).grouped(h, A, B, C, ends, G, T, N, K, lda, ldb, strideb, ldc, layoutB, dtype, stream)
+
+
+def gemm_grouped_wgrad_run(h, A, B, C, ends, G, T, M, N, lda, ldb, ldc, stridec, dtype, stream=None) -> int:
+    """Enqueue the gradient of the groups' matrices; returns the gemm_status code."""
+    return (_native or _bind()).grouped_wgrad(h, A, B, C, ends, G, T, M, N, lda, ldb, ldc, stridec, dtype, stream)
+
+
+def gemm_grouped_mxfp4_run(h, A, B, C, SA, SB, ends, G, T, N, K, lda, ldb, strideb, ldc, ldsa, ldsb, stridesb, dtype,
+                           stream=None) -> int:
+    """Enqueue each group's MXFP4 rows times the group's MXFP4 matrix; returns the gemm_status code."""
+    return (_native or _bind()).grouped_mxfp4(h, A, B, C, SA, SB, ends, G, T, N, K, lda, ldb, strideb, ldc, ldsa, ldsb,
+                                              stridesb, dtype, stream)
+
+
 def gemm_destroy(h) -> int:
     return load_library().gemm_destroy(h)
 
@@ -175,8 +219,7 @@ def gemm_status_str(status: int) -> str:
 class Library:
     """gemm_create, gemm_run, gemm_destroy and gemm_status_str bound to one
     specific build of the library (the default build, or an A/B build from
-    ablation_library()); the linear layer's entry points where the build has
-    them (the default build and "poison")."""
+    ablation_library()); the other entry points where the build has them (the default build and "poison")."""
 
     def __init__(self, path):
         self.path = path
@@ -212,6 +255,29 @@ class Library:
 
     def gemm_rmsnorm_run(self, h, X, R, W, H, Y, S, M, N, ldx, ldr, ldh, ldy, eps, dtype, stream=None) -> int:
         return self._layer("gemm_rmsnorm_run", h, (X, R, W, H, Y, S, M, N, ldx, ldr, ldh, ldy, eps, dtype), stream)
+
+    def gemm_mxfp4_quantize_run(self, h, X, Q, S, M, K, ldx, ldq, lds, layoutX, dtype, stream=None) -> int:
+        return self._layer("gemm_mxfp4_quantize_run", h, (X, Q, S, M, K, ldx, ldq, lds, layoutX, dtype), stream)
+
+    def gemm_mxfp4_dequantize_run(self, h, Q, S, Y, M, K, ldq, lds, ldy, dtype, stream=None) -> int:
+        return self._layer("gemm_mxfp4_dequantize_run", h, (Q, S, Y, M, K, ldq, lds, ldy, dtype), stream)
+
+    def gemm_mxfp4_run(self, h, A, B, C, SA, SB, M, N, K, lda, ldb, ldc, ldsa, ldsb, dtype, stream=None) -> int:
+        return self._layer("gemm_mxfp4_run", h, (A, B, C, SA, SB, M, N, K, lda, ldb, ldc, ldsa, ldsb, dtype), stream)
+
+    def gemm_grouped_run(self, h, A, B, C, ends, G, T, N, K, lda, ldb, strideb, ldc, layoutB, dtype,
+                         stream=None) -> int:
+        return self._layer("gemm_grouped_run", h, (A, B, C, ends, G, T, N, K, lda, ldb, strideb, ldc, layoutB, dtype),
+                           stream)
+
+    def gemm_grouped_wgrad_run(self, h, A, B, C, ends, G, T, M, N, lda, ldb, ldc, stridec, dtype, stream=None) -> int:
+        return self._layer("gemm_grouped_wgrad_run", h, (A, B, C, ends, G, T, M, N, lda, ldb, ldc, stridec, dtype),
+                           stream)
+
+    def gemm_grouped_mxfp4_run(self, h, A, B, C, SA, SB, ends, G, T, N, K, lda, ldb, strideb, ldc, ldsa, ldsb, stridesb,
+                               dtype, stream=None) -> int:
+        return self._layer("gemm_grouped_mxfp4_run", h, (A, B, C, SA, SB, ends, G, T, N, K, lda, ldb, strideb, ldc, ldsa,
+                                                         ldsb, stridesb, dtype), stream)
 
     def gemm_destroy(self, h) -> int:
         return self._lib.gemm_destroy(h)

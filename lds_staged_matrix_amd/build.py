@@ -22,7 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblds_gemm.so")
 BINDING = os.path.join(PKG, "_binding.so")
 ABLATION_DIR = os.path.join(PKG, "ablation")
-SOURCES = ["gemm_api.hip", "gemm_scaled.hip", "gemm_w4.hip", "gemm_norm.hip"]
+SOURCES = ["gemm_api.hip", "gemm_scaled.hip", "gemm_w4.hip", "gemm_norm.hip",
+           "gemm_grouped.hip", "gemm_mxfp4.hip", "gemm_mxfp4_convert.hip"]
 # Most A/B builds change gemm_run's kernels only; these change every kernel that uses LDS.
 VARIANT_SOURCES = ["gemm_api.hip"]
 WHOLE_VARIANTS = ("poison",)

@@ -27,6 +27,12 @@ static __typeof__(gemm_run) *p_run;
 static __typeof__(gemm_scaled_run) *p_scaled;
 static __typeof__(gemm_w4_run) *p_w4;
 static __typeof__(gemm_rmsnorm_run) *p_rmsnorm;
+static __typeof__(gemm_mxfp4_quantize_run) *p_mxfp4_quantize;
+static __typeof__(gemm_mxfp4_dequantize_run) *p_mxfp4_dequantize;
+static __typeof__(gemm_mxfp4_run) *p_mxfp4;
+static __typeof__(gemm_grouped_run) *p_grouped;
+static __typeof__(gemm_grouped_wgrad_run) *p_grouped_wgrad;
+static __typeof__(gemm_grouped_mxfp4_run) *p_grouped_mxfp4;
 static PyObject *s_data_ptr, *s_cuda_stream, *s_value;
 static PyObject *c_void_p, *c_cast;                 /* of ctypes */
 
@@ -192,23 +198,92 @@ static PyObject *py_rmsnorm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
        v.w[4], v.w[5], v.f[0], v.n[0], v.s);
 }
 
-static PyObject *py_bind(PyObject *self, PyObject *args) {
-  unsigned long long run, scaled, w4, rmsnorm;
+static PyObject *py_mxfp4_quantize(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  static const struct shape t = {"gemm_mxfp4_quantize_run", 3, 5, 0, 2, {"M", "K", "ldx", "ldq", "lds", "layoutX", "dtype"}};
+  struct values v;
   (void)self;
-  if (!PyArg_ParseTuple(args, "KKKK", &run, &scaled, &w4, &rmsnorm)) return NULL;
-  p_run = (__typeof__(p_run))(uintptr_t)run;
-  p_scaled = (__typeof__(p_scaled))(uintptr_t)scaled;
-  p_w4 = (__typeof__(p_w4))(uintptr_t)w4;
-  p_rmsnorm = (__typeof__(p_rmsnorm))(uintptr_t)rmsnorm;
+  if (take(&t, a, n, &v)) return NULL;
+  CALL(p_mxfp4_quantize, v.h, v.p[0], v.p[1], v.p[2], v.w[0], v.w[1], v.w[2], v.w[3], v.w[4], v.n[0], v.n[1], v.s);
+}
+
+static PyObject *py_mxfp4_dequantize(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  static const struct shape t = {"gemm_mxfp4_dequantize_run", 3, 5, 0, 1, {"M", "K", "ldq", "lds", "ldy", "dtype"}};
+  struct values v;
+  (void)self;
+  if (take(&t, a, n, &v)) return NULL;
+  CALL(p_mxfp4_dequantize, v.h, v.p[0], v.p[1], v.p[2], v.w[0], v.w[1], v.w[2], v.w[3], v.w[4], v.n[0], v.s);
+}
+
+static PyObject *py_mxfp4(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  static const struct shape t = {"gemm_mxfp4_run", 5, 8, 0, 1, {"M", "N", "K", "lda", "ldb", "ldc", "ldsa", "ldsb", "dtype"}};
+  struct values v;
+  (void)self;
+  if (take(&t, a, n, &v)) return NULL;
+  CALL(p_mxfp4, v.h, v.p[0], v.p[1], v.p[2], v.p[3], v.p[4], v.w[0], v.w[1], v.w[2], v.w[3], v.w[4], v.w[5], v.w[6],
+       v.w[7], v.n[0], v.s);
+}
+
+static PyObject *py_grouped(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  static const struct shape t = {"gemm_grouped_run", 4, 8, 0, 2,
+                                 {"G", "T", "N", "K", "lda", "ldb", "strideb", "ldc", "layoutB", "dtype"}};
+  struct values v;
+  (void)self;
+  if (take(&t, a, n, &v)) return NULL;
+  CALL(p_grouped, v.h, v.p[0], v.p[1], v.p[2], (const int32_t *)v.p[3], v.w[0], v.w[1], v.w[2], v.w[3], v.w[4], v.w[5],
+       v.w[6], v.w[7], v.n[0], v.n[1], v.s);
+}
+
+static PyObject *py_grouped_wgrad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  static const struct shape t = {"gemm_grouped_wgrad_run", 4, 8, 0, 1,
+                                 {"G", "T", "M", "N", "lda", "ldb", "ldc", "stridec", "dtype"}};
+  struct values v;
+  (void)self;
+  if (take(&t, a, n, &v)) return NULL;
+  CALL(p_grouped_wgrad, v.h, v.p[0], v.p[1], v.p[2], (const int32_t *)v.p[3], v.w[0], v.w[1], v.w[2], v.w[3], v.w[4],
+       v.w[5], v.w[6], v.w[7], v.n[0], v.s);
+}
+
+static PyObject *py_grouped_mxfp4(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  static const struct shape t = {
+      "gemm_grouped_mxfp4_run", 6, 11, 0, 1,
+      {"G", "T", "N", "K", "lda", "ldb", "strideb", "ldc", "ldsa", "ldsb", "stridesb", "dtype"}};
+  struct values v;
+  (void)self;
+  if (take(&t, a, n, &v)) return NULL;
+  CALL(p_grouped_mxfp4, v.h, v.p[0], v.p[1], v.p[2], v.p[3], v.p[4], (const int32_t *)v.p[5], v.w[0], v.w[1], v.w[2],
+       v.w[3], v.w[4], v.w[5], v.w[6], v.w[7], v.w[8], v.w[9], v.w[10], v.n[0], v.s);
+}
+
+static PyObject *py_bind(PyObject *self, PyObject *args) {
+  unsigned long long f[10];
+  (void)self;
+  if (!PyArg_ParseTuple(args, "KKKKKKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9]))
+    return NULL;
+  p_run = (__typeof__(p_run))(uintptr_t)f[0];
+  p_scaled = (__typeof__(p_scaled))(uintptr_t)f[1];
+  p_w4 = (__typeof__(p_w4))(uintptr_t)f[2];
+  p_rmsnorm = (__typeof__(p_rmsnorm))(uintptr_t)f[3];
+  p_mxfp4_quantize = (__typeof__(p_mxfp4_quantize))(uintptr_t)f[4];
+  p_mxfp4_dequantize = (__typeof__(p_mxfp4_dequantize))(uintptr_t)f[5];
+  p_mxfp4 = (__typeof__(p_mxfp4))(uintptr_t)f[6];
+  p_grouped = (__typeof__(p_grouped))(uintptr_t)f[7];
+  p_grouped_wgrad = (__typeof__(p_grouped_wgrad))(uintptr_t)f[8];
+  p_grouped_mxfp4 = (__typeof__(p_grouped_mxfp4))(uintptr_t)f[9];
   Py_RETURN_NONE;
 }
 
 static PyMethodDef methods[] = {
-    {"bind", py_bind, METH_VARARGS, "Addresses of gemm_run, gemm_scaled_run, gemm_w4_run, gemm_rmsnorm_run."},
+    {"bind", py_bind, METH_VARARGS, "Addresses of the entry points that enqueue work, in the header's order."},
     {"run", (PyCFunction)(void (*)(void))py_run, METH_FASTCALL, "gemm_run"},
     {"scaled", (PyCFunction)(void (*)(void))py_scaled, METH_FASTCALL, "gemm_scaled_run"},
     {"w4", (PyCFunction)(void (*)(void))py_w4, METH_FASTCALL, "gemm_w4_run"},
     {"rmsnorm", (PyCFunction)(void (*)(void))py_rmsnorm, METH_FASTCALL, "gemm_rmsnorm_run"},
+    {"mxfp4_quantize", (PyCFunction)(void (*)(void))py_mxfp4_quantize, METH_FASTCALL, "gemm_mxfp4_quantize_run"},
+    {"mxfp4_dequantize", (PyCFunction)(void (*)(void))py_mxfp4_dequantize, METH_FASTCALL, "gemm_mxfp4_dequantize_run"},
+    {"mxfp4", (PyCFunction)(void (*)(void))py_mxfp4, METH_FASTCALL, "gemm_mxfp4_run"},
+    {"grouped", (PyCFunction)(void (*)(void))py_grouped, METH_FASTCALL, "gemm_grouped_run"},
+    {"grouped_wgrad", (PyCFunction)(void (*)(void))py_grouped_wgrad, METH_FASTCALL, "gemm_grouped_wgrad_run"},
+    {"grouped_mxfp4", (PyCFunction)(void (*)(void))py_grouped_mxfp4, METH_FASTCALL, "gemm_grouped_mxfp4_run"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -1,0 +1,143 @@
+// gemm_grouped.hip -- gemm_grouped_run: the rows of each group (expert) times the
+// group's own matrix, and gemm_grouped_wgrad_run: the gradient of those matrices.
+//
+//   C[t][n]    = sum_k A[t][k] * B[g][k][n]         for t in group g
+//   C[g][m][n] = sum over t in group g of A[t][m] * B[t][n]
+//
+// The gradient of the rows is the first of them with B's other layout.  The
+// kernels are those of gemm_kernel_tile256.h and gemm_kernel_tile.h.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gemm_tile_launch.h"
+
+namespace lsm {
+
+using Tile128 = TileShape<128, 128, 2, 2, 2>;
+using Stream16 = StreamShape<16, 32, 8, 3>;
+using Stream32 = StreamShape<32, 32, 8, 2>;
+using Stream16MN = StreamShape<16, 128, 4, 2>;
+using Stream32MN = StreamShape<32, 128, 4, 2>;
+
+template <int LB, int IN, int OUT>
+static hipError_t dispatch_rows(const TileArgs &p, hipStream_t s) {
+  const int64_t mean = ceil_div(p.M, p.G);
+  if (mean <= 16) return launch_stream<std::conditional_t<LB == KC, Stream16, Stream16MN>, GROUP_ROWS, LB, IN, OUT>(p, s);
+  if (mean <= 32) return launch_stream<std::conditional_t<LB == KC, Stream32, Stream32MN>, GROUP_ROWS, LB, IN, OUT>(p, s);
+  if (mean >= 192 && workgroups<GROUP_ROWS>(p, 256, 256) >= 256)
+    return launch_tile256<GROUP_ROWS, KC, LB, IN, OUT>(p, s);
+  return launch_tile<Tile128, GROUP_ROWS, KC, LB, IN, OUT>(p, s);
+}
+
+template <int IN, int OUT>
+static hipError_t dispatch_sums(const TileArgs &p, hipStream_t s) {
+  if (workgroups<GROUP_SUMS>(p, 256, 256) >= 256) return launch_tile256<GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
+  return launch_tile<Tile128, GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
+}
+
+template <class F>
+static hipError_t with_types(int dtype, F call) {
+  constexpr std::integral_constant<int, IN_BF16> bf16{};
+  constexpr std::integral_constant<int, IN_F16> f16{};
+  constexpr std::integral_constant<int, OUT_F32> f32{};
+  switch (dtype) {
+    case GEMM_BF16_F32: return call(bf16, f32);
+    case GEMM_BF16_BF16: return call(bf16, std::integral_constant<int, OUT_BF16>{});
+    case GEMM_F16_F16: return call(f16, std::integral_constant<int, OUT_F16>{});
+    default: return call(f16, f32);
+  }
+}
+
+// The smallest tiles, of 16 x 32, must fit a launch of fewer than 2^32 threads of 512 each.
+template <int MODE>
+static bool launch_fits(int64_t M, int64_t N, int64_t G) {
+  const int64_t tm = MODE == GROUP_ROWS ? most_row_tiles(M, G, 16, 1) : ceil_div(M, 128) * G;
+  int64_t n;
+  return !__builtin_mul_overflow(tm, ceil_div(N, MODE == GROUP_ROWS ? 32 : 128), &n) && n < ((int64_t)1 << 23);
+}
+
+}  // namespace lsm
+
+extern "C" int gemm_grouped_run(gemm_handle_t h, const void *A, const void *B, void *C, const int32_t *ends, int64_t G,
+                                int64_t T, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t strideb,
+                                int64_t ldc, int layoutB, int dtype, hipStream_t stream) {
+  using namespace lsm;
+  if (!h || G < 0 || T < 0 || N < 0 || K < 0 || dtype < GEMM_BF16_F32 || dtype > GEMM_F16_F32) return GEMM_ERR_INVALID_ARG;
+  if (layoutB != GEMM_K_CONTIG && layoutB != GEMM_MN_CONTIG) return GEMM_ERR_INVALID_ARG;
+  if (G == 0 || T == 0 || N == 0) return GEMM_OK;
+  const bool kc = layoutB == GEMM_K_CONTIG;
+  if (!C || !ends || (K > 0 && (!A || !B))) return GEMM_ERR_INVALID_ARG;
+  if (ldc < N || (K > 0 && (lda < K || ldb < (kc ? K : N) || strideb < 0))) return GEMM_ERR_INVALID_ARG;
+
+  const bool out_f32 = dtype == GEMM_BF16_F32 || dtype == GEMM_F16_F32;
+  if (G >= kTileMaxDim || T >= kTileMaxDim || N >= kTileMaxDim || K >= kTileMaxDim || ldc >= kTileMaxLd)
+    return GEMM_ERR_UNSUPPORTED;
+  if (((uintptr_t)C & (out_f32 ? 3 : 1)) || ((uintptr_t)ends & 3)) return GEMM_ERR_UNSUPPORTED;
+  if (K > 0) {
+    if (2 * lda >= kTileMaxPitch || ldb >= kTileMaxPitch / 2 || strideb >= kTileMaxLd) return GEMM_ERR_UNSUPPORTED;
+    if (((uintptr_t)A & 15) || ((uintptr_t)B & 15) || lda % 8 || ldb % 8 || strideb % 8) return GEMM_ERR_UNSUPPORTED;
+    if (K % 8 || (!kc && N % 8)) return GEMM_ERR_UNSUPPORTED;
+  }
+  if (!launch_fits<GROUP_ROWS>(T, N, G)) return GEMM_ERR_UNSUPPORTED;
+  const int64_t c_bytes = footprint_bytes(T, ldc, N, out_f32 ? 4 : 2);
+  const int64_t a_bytes = K > 0 ? footprint_bytes(T, lda, K, 2) : 0;
+  const int64_t b_bytes = K > 0 ? stacked_bytes(G, 2 * strideb, kc ? footprint_bytes(N, ldb, K, 2) : footprint_bytes(K, ldb, N, 2)) : 0;
+  if (c_bytes < 0 || a_bytes < 0 || b_bytes < 0) return GEMM_ERR_UNSUPPORTED;
+  if (overlaps_any({C, c_bytes}, {{A, a_bytes}, {B, b_bytes}, {ends, 4 * G}})) return GEMM_ERR_INVALID_ARG;
+
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess || dev != h->device) return GEMM_ERR_DEVICE;
+  TileArgs p{};
+  p.A = (const char *)A, p.B = (const char *)B, p.C = C, p.ends = ends, p.G = (int)G;
+  p.M = (int)T, p.N = (int)N, p.K = (int)K;
+  p.lda = 2 * lda, p.ldb = 2 * ldb, p.strideb = 2 * strideb, p.ldc = ldc;
+  p.c_vec = (uintptr_t)C % 16 == 0 && ldc * (out_f32 ? 4 : 2) % 16 == 0;
+  const hipError_t e = with_types(dtype, [&](auto in, auto out) {
+    constexpr int IN = decltype(in)::value, OUT = decltype(out)::value;
+    return kc ? dispatch_rows<KC, IN, OUT>(p, stream) : dispatch_rows<MNC, IN, OUT>(p, stream);
+  });
+  return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+extern "C" int gemm_grouped_wgrad_run(gemm_handle_t h, const void *A, const void *B, void *C, const int32_t *ends,
+                                      int64_t G, int64_t T, int64_t M, int64_t N, int64_t lda, int64_t ldb, int64_t ldc,
+                                      int64_t stridec, int dtype, hipStream_t stream) {
+  using namespace lsm;
+  if (!h || G < 0 || T < 0 || M < 0 || N < 0 || dtype < GEMM_BF16_F32 || dtype > GEMM_F16_F32) return GEMM_ERR_INVALID_ARG;
+  if (G == 0 || M == 0 || N == 0) return GEMM_OK;
+  if (!C || !ends || (T > 0 && (!A || !B))) return GEMM_ERR_INVALID_ARG;
+  if (ldc < N || (T > 0 && (lda < M || ldb < N))) return GEMM_ERR_INVALID_ARG;
+
+  const bool out_f32 = dtype == GEMM_BF16_F32 || dtype == GEMM_F16_F32;
+  const int64_t size = out_f32 ? 4 : 2;
+  if (G >= kTileMaxDim || T >= kTileMaxDim || M >= kTileMaxDim || N >= kTileMaxDim || ldc >= kTileMaxLd)
+    return GEMM_ERR_UNSUPPORTED;
+  if (((uintptr_t)C & (uintptr_t)(size - 1)) || ((uintptr_t)ends & 3)) return GEMM_ERR_UNSUPPORTED;
+  if (T > 0) {
+    if (2 * lda >= kTileMaxPitch || 2 * ldb >= kTileMaxPitch) return GEMM_ERR_UNSUPPORTED;
+    if (((uintptr_t)A & 15) || ((uintptr_t)B & 15) || lda % 8 || ldb % 8 || M % 8 || N % 8) return GEMM_ERR_UNSUPPORTED;
+  }
+  if (!launch_fits<GROUP_SUMS>(M, N, G)) return GEMM_ERR_UNSUPPORTED;
+  const int64_t one = footprint_bytes(M, ldc, N, size);
+  if (one < 0) return GEMM_ERR_UNSUPPORTED;
+  // the groups' results are disjoint
+  if (G > 1 && (stridec < 0 || stridec < one / size)) return GEMM_ERR_INVALID_ARG;
+  if (G > 1 && stridec >= ((int64_t)1 << 60)) return GEMM_ERR_UNSUPPORTED;
+  const int64_t c_bytes = stacked_bytes(G, G > 1 ? size * stridec : 0, one);
+  const int64_t a_bytes = T > 0 ? footprint_bytes(T, lda, M, 2) : 0, b_bytes = T > 0 ? footprint_bytes(T, ldb, N, 2) : 0;
+  if (c_bytes < 0 || a_bytes < 0 || b_bytes < 0) return GEMM_ERR_UNSUPPORTED;
+  if (overlaps_any({C, c_bytes}, {{A, a_bytes}, {B, b_bytes}, {ends, 4 * G}})) return GEMM_ERR_INVALID_ARG;
+
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess || dev != h->device) return GEMM_ERR_DEVICE;
+  TileArgs p{};
+  p.A = (const char *)A, p.B = (const char *)B, p.C = C, p.ends = ends, p.G = (int)G;
+  p.M = (int)M, p.N = (int)N, p.K = (int)T;
+  p.lda = 2 * lda, p.ldb = 2 * ldb, p.ldc = ldc, p.stridec = G > 1 ? stridec : 0;
+  p.c_vec = (uintptr_t)C % 16 == 0 && ldc * size % 16 == 0 && p.stridec * size % 16 == 0;
+  const hipError_t e = with_types(dtype, [&](auto in, auto out) {
+    return dispatch_sums<decltype(in)::value, decltype(out)::value>(p, stream);
+  });
+  return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
