@@ -14,26 +14,66 @@
 
 namespace lsm {
 
+// Tiles: rows x columns, waves, LDS stages, groups of waves that share K.  Streams:
+// rows x columns, waves, stages a wave.
 using Tile128 = TileShape<128, 128, 2, 2, 2>;
-using Stream16 = StreamShape<16, 32, 8, 3>;
-using Stream32 = StreamShape<32, 32, 8, 2>;
-using Stream16MN = StreamShape<16, 128, 4, 2>;
-using Stream32MN = StreamShape<32, 128, 4, 2>;
+using Tile128Alone = TileShape<128, 128, 2, 4, 3>;
+using Tile64 = TileShape<64, 128, 2, 2, 2>;
+using Tile64SplitK = TileShape<64, 128, 2, 2, 3, 2>;
+using SmallSplitK = TileShape<64, 64, 2, 2, 3, 2>;
+using SmallSplitKMN = TileShape<32, 128, 1, 4, 3, 2>;
+using Stream16 = StreamShape<16, 64, 4, 2>;
+using Stream32 = StreamShape<32, 64, 4, 2>;
+using Stream16MN = StreamShape<16, 128, 2, 3>;
+using Stream32MN = StreamShape<32, 128, 2, 2>;
 
+// By the mean number of rows a group, and by how many tiles are to be expected
+// against the 256 CUs.  Times of uneven groups in bf16, B K- and MN-contiguous
+// (rows, groups, N, K):
+//  * streams up to 32 rows (64, 16, 4096, 4096: 84 and 94 us; 240, 8, 4096, 4096: 58
+//    and 69, as 128 x 128 tiles 69 and 62);
+//  * the 256 x 256 tile and its halves and quarters from 192 rows on (2048, 8, 4096,
+//    4096: 95 and 88 us, as 128 x 128 tiles 125; 16384, 8, 4096, 4096: 435 and 429, 590;
+//    but 1024, 8, 4096, 4096: 84 and 78, 74 and 78);
+//  * few tiles share K out over two groups of waves: 64 x 128 (1500, 8, 896, 1152: 11.9
+//    and 11.7 us; with one group 14.2), fewer still 64 x 64 or 32 x 128 (700, 8, 1152,
+//    896: 8.7 and 8.8; as 64 x 128 10.3);
+//  * tiles of 128 x 128 that are about as many as the CUs stand alone on one, with
+//    three stages (300, 8, 4096, 4096: 50 and 49 us, as 64 x 128 72); more of them go two
+//    to a CU (1024, 8, 4096, 4096: 74 and 78, alone 84 and 83), and those of up to 96
+//    rows are 64 x 128 (2048, 32, 1152, 896: 20.5 and 20.0, as 128 x 128 23.0 and 22.6).
 template <int LB, int IN, int OUT>
 static hipError_t dispatch_rows(const TileArgs &p, hipStream_t s) {
   const int64_t mean = ceil_div(p.M, p.G);
   if (mean <= 16) return launch_stream<std::conditional_t<LB == KC, Stream16, Stream16MN>, GROUP_ROWS, LB, IN, OUT>(p, s);
   if (mean <= 32) return launch_stream<std::conditional_t<LB == KC, Stream32, Stream32MN>, GROUP_ROWS, LB, IN, OUT>(p, s);
-  if (mean >= 192 && workgroups<GROUP_ROWS>(p, 256, 256) >= 256)
-    return launch_tile256<GROUP_ROWS, KC, LB, IN, OUT>(p, s);
+  if (mean >= 192 && expected_tiles(p, 256, 256) >= 128) return launch_tile256<GROUP_ROWS, KC, LB, IN, OUT>(p, s);
+  if (expected_tiles(p, 64, 128) < 160)
+    return launch_tile<std::conditional_t<LB == KC, SmallSplitK, SmallSplitKMN>, GROUP_ROWS, KC, LB, IN, OUT>(p, s);
+  const int64_t tiles = expected_tiles(p, 128, 128);
+  if (tiles < 192) return launch_tile<Tile64SplitK, GROUP_ROWS, KC, LB, IN, OUT>(p, s);
+  if (tiles <= 264) return launch_tile<Tile128Alone, GROUP_ROWS, KC, LB, IN, OUT>(p, s);
+  if (mean <= 96) return launch_tile<Tile64, GROUP_ROWS, KC, LB, IN, OUT>(p, s);
   return launch_tile<Tile128, GROUP_ROWS, KC, LB, IN, OUT>(p, s);
 }
 
+// The 256 x 256 tile where it fills the CUs and its sums are 512 rows long or more
+// in the mean (bf16 to fp32; rows, groups, M, N: 16384, 8, 4096, 4096: 485 us, as 128 x
+// 128 tiles 597; 4096, 8, 2048, 2048: 54 and 57; but 1000, 8, 4096, 4096: 131 and 112).
+// 128 x 128 tiles of which a CU has one or none have three stages (16384, 4, 1024,
+// 1024: 72 us, with two 102), few of them two groups of waves that share the sum out
+// (8192, 2, 512, 512: 47 us; 54 without).
+using Tile128Sums = TileShape<128, 128, 2, 4, 2>;
+using Tile128SplitK = TileShape<128, 128, 2, 2, 2, 2>;
+
 template <int IN, int OUT>
 static hipError_t dispatch_sums(const TileArgs &p, hipStream_t s) {
-  if (workgroups<GROUP_SUMS>(p, 256, 256) >= 256) return launch_tile256<GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
-  return launch_tile<Tile128, GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
+  if (ceil_div(p.K, p.G) >= 512 && workgroups<GROUP_SUMS>(p, 256, 256) >= 256)
+    return launch_tile256<GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
+  const int64_t tiles = workgroups<GROUP_SUMS>(p, 128, 128);
+  if (tiles <= 128) return launch_tile<Tile128SplitK, GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
+  if (tiles <= 256) return launch_tile<Tile128Alone, GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
+  return launch_tile<Tile128Sums, GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
 }
 
 template <class F>

@@ -4,9 +4,8 @@
 // behind group g's last, and group g starts where the groups before it end.  No
 // host ever reads the ends, so a launch holds as many workgroups as any ends
 // could ask for, and each finds its own tile in them: every wave reads all the
-// ends, 64 at a time, and scans them in registers (two or three microseconds
-// less than a launch of its own that would write a list of tiles).  A workgroup
-// past the last tile leaves at once.
+// ends, 64 at a time, and scans them in registers.  A workgroup past the last
+// tile leaves at once.
 //
 // Whatever the ends hold, the groups found are disjoint, in order and inside the
 // T rows: an end counts as no less than the ends before it and no more than T.
@@ -81,19 +80,52 @@ struct GroupChunk {
   }
 };
 
+// A workgroup's part of the work: a tile, or one of `parts` equal shares of its
+// rows.
+struct Part {
+  int tile, sub, parts;
+};
+
+// The last `rest` tiles that do not fill the 256 CUs once more are cut into up to
+// MOST parts each, as many as still fit one round: a large tile takes long, and a
+// round of few of them as long as a full one (see gemm_kernel_tile256.h).
+constexpr int kCUs = 256;
+__host__ __device__ constexpr int rest_parts(int rest, int most) {
+  return most >= 4 && 4 * rest <= kCUs ? 4 : most >= 2 && 2 * rest <= kCUs ? 2 : 1;
+}
+template <int MOST>
+__device__ __forceinline__ bool part_of(int bid, int total, Part &w) {
+  w = {bid, 0, 1};
+  if constexpr (MOST == 1) return bid < total;
+  const int rest = total % kCUs, full = total - rest;
+  if (bid < full) return true;
+  w.parts = rest_parts(rest, MOST);
+  const int j = bid - full;
+  if (j >= rest * w.parts) return false;
+  w.sub = j / rest, w.tile = full + j - w.sub * rest;
+  return true;
+}
+// Workgroups of `total` tiles, or of no more than that many.
+constexpr int64_t workgroups_in_parts(int64_t total, int most, bool exact) {
+  if (most == 1) return total;
+  if (!exact) return total + kCUs * 3 / 4;             // 64 tiles in four parts, 128 in two
+  const int64_t rest = total % kCUs;
+  return total - rest + rest * rest_parts((int)rest, most);
+}
+
 // Workgroup `bid`'s group and its tile there, of BM rows by one of `tiles_n`
 // columns; false past the last tile.  Tiles are numbered group by group, and
 // each XCD has one contiguous range of the numbers.
-template <int BM, int ALIGN>
+template <int BM, int ALIGN, int MOST>
 __device__ __forceinline__ bool find_row_tile(const int32_t *ends, int G, int T, int tiles_n, int group_m, int bid,
-                                              int lane, Group &at, int &tm, int &tn) {
+                                              int lane, Group &at, Part &part, int &tm, int &tn) {
   const int chunks = (G + 63) / 64;
   uint32_t end = 0, count = 0;
   GroupChunk<BM, ALIGN> s(ends, G, T, 0, lane, end, count);
   for (int c = 1; c < chunks; c++) GroupChunk<BM, ALIGN>(ends, G, T, c, lane, end, count);
   const int total = (int)count * tiles_n;
-  if (bid >= total) return false;
-  const int id = xcd_logical_id(bid, total), q = id / tiles_n;
+  if (!part_of<MOST>(bid, total, part)) return false;
+  const int id = xcd_logical_id(part.tile, total), q = id / tiles_n;
   end = count = 0;
   for (int c = 0;; c++) {
     if (c > 0 || chunks > 1) s = GroupChunk<BM, ALIGN>(ends, G, T, c, lane, end, count);

@@ -2,7 +2,9 @@
 //
 // lds_gemm_tile_kernel: WM x WN waves on one tile of BM x BN; a K tile (128
 // bytes of either operand's rows, see gemm_tile.h) comes into one of NS LDS
-// stages, NS - 1 of them in flight, one barrier a K tile.
+// stages, NS - 1 of them in flight, one barrier a K tile.  With WK > 1 so many
+// groups of waves take turns at the K tiles, each with stages of its own: for
+// tiles too few to fill the chip, whose time is the length of the K loop.
 //
 // lds_gemm_stream_kernel: few rows, so that the time is that of reading B once.
 // The workgroup's waves split K, slab by slab of 128 bytes, and each keeps a ring
@@ -113,15 +115,16 @@ __device__ __forceinline__ void tile_mfma(v4f32 (&acc)[FM][FN], const v8i16 (&a)
 
 // ------------------------------------------------------------------- tiles
 
-template <int BM_, int BN_, int WM_, int WN_, int NS_>
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int WK_ = 1>
 struct TileShape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, NT = 64 * WM * WN, GROUP_M = 8;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, WK = WK_, GROUP_M = 8;
+  static constexpr int NT = 64 * WM * WN;                // of one group
 };
 
 template <class S, int MODE, int LA, int LB, int IN, int OUT>
-__global__ __launch_bounds__(S::NT, 2) void lds_gemm_tile_kernel(const TileArgs p) {
+__global__ __launch_bounds__(S::NT * S::WK, 2) void lds_gemm_tile_kernel(const TileArgs p) {
   constexpr bool MX = IN == IN_MXFP4;
-  constexpr int BM = S::BM, BN = S::BN, NS = S::NS, NT = S::NT, EB = MX ? 1 : 2;
+  constexpr int BM = S::BM, BN = S::BN, NS = S::NS, NT = S::NT, WK = S::WK, EB = MX ? 1 : 2;
   constexpr int TM = BM / S::WM, TN = BN / S::WN, FM = TM / 16, FN = TN / 16, KSTEPS = 2;
   using OA = OperandTile<BM, kTileBytes / EB, LA, NT, EB, 1>;
   using OB = OperandTile<BN, kTileBytes / EB, LB, NT, EB, 1>;
@@ -130,30 +133,35 @@ __global__ __launch_bounds__(S::NT, 2) void lds_gemm_tile_kernel(const TileArgs 
   constexpr int SA_AT = OA::BYTES + OB::BYTES, SB_AT = SA_AT + GA::BYTES;
   constexpr int STAGE = SA_AT + (MX ? (GA::BYTES + GB::BYTES + 1023) / 1024 * 1024 : 0);
   constexpr int LPT = OA::LOADS + OB::LOADS, SCALE_LOADS = MX ? GA::INSTS + GB::INSTS : 0;
-  constexpr int LDS_BYTES = NS * STAGE > BM * BN * 4 ? NS * STAGE : BM * BN * 4;
+  constexpr int LDS_BYTES = WK * (NS * STAGE > BM * BN * 4 ? NS * STAGE : BM * BN * 4);
   static_assert(SCALE_LOADS <= S::WM * S::WN && (NS - 2) * (LPT + 1) < 64 && LDS_BYTES <= 160 * 1024, "stages");
   __shared__ __attribute__((aligned(1024))) char smem[LDS_BYTES];
 
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x & (NT - 1), lane = tid & 63;
   if constexpr (LSM_LDS_POISON) {   // poison build: all of LDS, before any load or write
-    lds_poison(smem, LDS_BYTES, tid, NT);
+    lds_poison(smem, LDS_BYTES, threadIdx.x, NT * WK);
     __syncthreads();
   }
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wk = WK == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
   const int wm = wave / S::WN, wn = wave % S::WN;
   Where w{};
   if (!locate<BM, BN, S::GROUP_M, MODE, LA, LB, IN, 1>(p, lane, w)) return;
   const int KT = (w.K + kTileK(IN) - 1) / kTileK(IN);
   const int kbytes = MX ? w.K / 2 : 2 * w.K;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem;
+  char *stages = smem + wk * NS * STAGE;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)stages;
   const Loader<OA, NT> la(tid, w.a, p.lda, LA == KC ? w.rows : 2 * w.rows, LA == KC ? kbytes : w.K);
   const Loader<OB, NT> lb(tid, w.b, p.ldb, LB == KC ? w.cols : 2 * w.cols, LB == KC ? kbytes : w.K);
   const GA sa(w.sa, p.ldsa, w.rows, w.K / kMxBlock);
   const GB sb(w.sb, p.ldsb, w.cols, w.K / kMxBlock);
 
-  // K tile kt into stage `st`; behind the last, zeros, so that a K tile is
-  // always as many loads.
-  auto issue = [&](int kt, int st) {
+  // The group's K tile i, counted from the XCD's start, into stage `st`; behind the
+  // last, zeros, so that a K tile is always as many loads.
+  const int start = LA == KC ? (int)((uint32_t)(blockIdx.x & 7) * (uint32_t)KT >> 3) : 0;
+  auto issue = [&](int i, int st) {
+    const int at_k = i * WK + wk, on = at_k + start;
+    const int kt = at_k >= KT ? KT : on < KT ? on : on - KT;
     const uint32_t at = lds0 + (uint32_t)(st * STAGE);
     const auto ra = la.at(kt, kbytes);
     const auto rb = lb.at(kt, kbytes);
@@ -179,28 +187,28 @@ __global__ __launch_bounds__(S::NT, 2) void lds_gemm_tile_kernel(const TileArgs 
 #pragma unroll
     for (int t = 0; t < NS - 1; t++) issue(t, t);
     int st = 0, free = NS - 1;
-    for (int kt = 0; kt < KT; ++kt) {
-      // K tile kt landed (this wave's part: NS - 2 later ones may be in flight) ...
+    for (int i = 0; i * WK < KT; ++i) {
+      // the group's K tile i landed (this wave's part: NS - 2 later ones may be in flight) ...
       if (wave < SCALE_LOADS)
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * (LPT + 1)) : "memory");
       else
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * LPT) : "memory");
       __syncthreads();                                   // ... every wave's, and the stage before it is read
-      issue(kt + NS - 1, free);
-      const char *sA = smem + st * STAGE, *sB = sA + OA::BYTES;
+      issue(i + NS - 1, free);
+      const char *sA = stages + st * STAGE, *sB = sA + OA::BYTES;
 #pragma unroll
       for (int kk = 0; kk < KSTEPS; kk++) {
         v8i16 fa[FM], fb[FN];
         int ga[FM], gb[FN];
 #pragma unroll
-        for (int i = 0; i < FM; i++) {
-          fa[i] = read_frag16<OA>(sA, lane, wm * TM + 16 * i, kk);
-          ga[i] = MX ? sa.read(smem + st * STAGE + SA_AT, 4 * kk + (lane >> 4), wm * TM + 16 * i + (lane & 15)) : 0;
+        for (int q = 0; q < FM; q++) {
+          fa[q] = read_frag16<OA>(sA, lane, wm * TM + 16 * q, kk);
+          ga[q] = MX ? sa.read(sA + SA_AT, 4 * kk + (lane >> 4), wm * TM + 16 * q + (lane & 15)) : 0;
         }
 #pragma unroll
-        for (int j = 0; j < FN; j++) {
-          fb[j] = read_frag16<OB>(sB, lane, wn * TN + 16 * j, kk);
-          gb[j] = MX ? sb.read(smem + st * STAGE + SB_AT, 4 * kk + (lane >> 4), wn * TN + 16 * j + (lane & 15)) : 0;
+        for (int q = 0; q < FN; q++) {
+          fb[q] = read_frag16<OB>(sB, lane, wn * TN + 16 * q, kk);
+          gb[q] = MX ? sb.read(sA + SB_AT, 4 * kk + (lane >> 4), wn * TN + 16 * q + (lane & 15)) : 0;
         }
         tile_mfma<IN>(acc, fa, fb, ga, gb);
       }
@@ -209,7 +217,7 @@ __global__ __launch_bounds__(S::NT, 2) void lds_gemm_tile_kernel(const TileArgs 
     }
     wait_dma();                                          // no load still targets the LDS
   }
-  add_and_store<BM, BN, 1, OUT>(p.C, acc, smem, w, p.ldc, 0, wm * TM, wn * TN, lane, NT);
+  add_and_store<BM, BN, WK, OUT>(p.C, acc, smem, w, p.ldc, wk, wm * TM, wn * TN, lane, NT * WK);
 }
 
 // ------------------------------------------------------------------ streams
@@ -243,7 +251,7 @@ __global__ __launch_bounds__(64 * S::WAVES, 2) void lds_gemm_stream_kernel(const
   using GA = ScaleTile<BM, MODE == GROUP_ROWS>;
   using GB = ScaleTile<BN, false>;
   constexpr int SA_AT = OA::BYTES + OB::BYTES, SB_AT = SA_AT + GA::BYTES;
-  constexpr int SLAB = SA_AT + (MX ? (GA::BYTES + GB::BYTES + 1023) / 1024 * 1024 : 0);
+  constexpr int SLAB = SA_AT + (MX ? GA::BYTES + GB::BYTES : 0);
   constexpr int LOADS = OA::LOADS + OB::LOADS + (MX ? GA::INSTS + GB::INSTS : 0);
   constexpr int LDS_BYTES = WAVES * (NS * SLAB > BM * BN * 4 ? NS * SLAB : BM * BN * 4);
   static_assert((NS - 1) * LOADS < 64 && LDS_BYTES <= 160 * 1024, "rings");

@@ -14,24 +14,73 @@
 
 namespace lsm {
 
-using MxTile64 = TileShape<64, 64, 2, 2, 4>;
+// Shapes as in gemm_grouped.hip.
 using MxTile128 = TileShape<128, 128, 2, 2, 2>;
-using MxStream16x16 = StreamShape<16, 16, 8, 3>;
-using MxStream16 = StreamShape<16, 32, 8, 2>;
-using MxStream32 = StreamShape<32, 32, 8, 2>;
+using MxTile128Alone = TileShape<128, 128, 2, 4, 3>;
+using MxTile64 = TileShape<64, 128, 2, 2, 2>;
+using MxTile64SplitK = TileShape<64, 128, 2, 2, 3, 2>;
+using MxSmallSplitK = TileShape<64, 64, 2, 2, 3, 2>;
+using MxTile32SplitK = TileShape<32, 64, 1, 2, 3, 2>;
+using MxStream16x16 = StreamShape<16, 16, 4, 2>;
+using MxStream16x32 = StreamShape<16, 32, 4, 2>;
+using MxStream16 = StreamShape<16, 64, 2, 2>;
+using MxStream32x32 = StreamShape<32, 32, 4, 2>;
+using MxStream32 = StreamShape<32, 64, 2, 2>;
+
+// Streams up to 32 rows, of the widest tiles that give every CU one (1 x 16384 x
+// 8192: 16.1 us in 64 columns, 18.0 in 16; 1 x 4096 x 4096: 5.6 in 16, 6.1 in 32; uneven
+// groups, rows, groups, N, K: 64, 16, 4096, 4096: 30.0 in 64 and 32, 37.5 in 16; 240, 8, 4096,
+// 4096: 20.7, as 128 x 128 tiles 24).
+template <int MODE, int OUT>
+static hipError_t dispatch_mx_stream(const TileArgs &p, int64_t rows, int64_t groups, hipStream_t s) {
+  const int64_t wide = groups * ceil_div(p.N, 64), half = groups * ceil_div(p.N, 32);
+  if (rows > 16)
+    return wide >= 256 ? launch_stream<MxStream32, MODE, KC, IN_MXFP4, OUT>(p, s)
+                       : launch_stream<MxStream32x32, MODE, KC, IN_MXFP4, OUT>(p, s);
+  if (wide >= 256) return launch_stream<MxStream16, MODE, KC, IN_MXFP4, OUT>(p, s);
+  if (half >= 256) return launch_stream<MxStream16x32, MODE, KC, IN_MXFP4, OUT>(p, s);
+  return launch_stream<MxStream16x16, MODE, KC, IN_MXFP4, OUT>(p, s);
+}
+
+// One product of more rows: the 256 x 256 tile, whole or in parts, where 128 x 128
+// would fill the CUs (1024 x 8192 x 8192 41 us, as 128 x 128 tiles 47; 1024 x 4096 x
+// 4096 18.1 and 18.4; 512 x 16384 x 4096 24.1 and 29.0); with fewer tiles two groups of
+// waves share K out (256 x 8192 x 8192 21.0 us in 64 x 128, without 32.8; 64 x 16384 x
+// 8192 17.5 in 64 x 64, 22.4 in 64 x 128; 128 x 4096 x 4096 8.4 in 32 x 64, 9.8 in 64 x 64),
+// and up to 64 rows of few columns are streamed (64 x 4096 x 4096 6.7 and 8.3).
+template <int OUT>
+static hipError_t dispatch_mx_one(const TileArgs &p, hipStream_t s) {
+  const auto tiles = [&](int bm, int bn) { return ceil_div(p.M, bm) * ceil_div(p.N, bn); };
+  if (p.M <= 32 || (p.M <= 64 && tiles(32, 32) <= 256)) return dispatch_mx_stream<GROUP_NONE, OUT>(p, p.M, 1, s);
+  if (tiles(128, 128) >= 256) return launch_tile256<GROUP_NONE, KC, KC, IN_MXFP4, OUT>(p, s);
+  if (tiles(64, 64) <= 128) return launch_tile<MxTile32SplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>(p, s);
+  if (tiles(64, 64) <= 256) return launch_tile<MxSmallSplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>(p, s);
+  return launch_tile<MxTile64SplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>(p, s);
+}
+
+// Groups of more rows: as for 16-bit rows (dispatch_rows in gemm_grouped.hip; rows,
+// groups, N, K: 2048, 8, 4096, 4096: 38.8 us in 256 x 256, 46 in 128 x 128; 1024, 8, 4096,
+// 4096: 36 and 28; 300, 8, 4096, 4096: 20.0 in 128 x 128 alone, 23.8 in two to a CU; 2048, 32,
+// 1152, 896: 9.9 in 64 x 128, 12.4 in 128 x 128).
+template <int OUT>
+static hipError_t dispatch_mx_groups(const TileArgs &p, hipStream_t s) {
+  const int64_t mean = ceil_div(p.M, p.G);
+  if (mean <= 32) return dispatch_mx_stream<GROUP_ROWS, OUT>(p, mean, p.G < p.M ? p.G : p.M, s);
+  if (mean >= 192 && expected_tiles(p, 256, 256) >= 128)
+    return launch_tile256<GROUP_ROWS, KC, KC, IN_MXFP4, OUT>(p, s);
+  if (expected_tiles(p, 64, 128) < 160) return launch_tile<MxSmallSplitK, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>(p, s);
+  const int64_t tiles = expected_tiles(p, 128, 128);
+  if (tiles >= 192 && tiles <= 264) return launch_tile<MxTile128Alone, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>(p, s);
+  if (tiles < 192 || mean <= 96) return launch_tile<MxTile64, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>(p, s);
+  return launch_tile<MxTile128, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>(p, s);
+}
 
 template <int MODE, int OUT>
 static hipError_t dispatch_mx(const TileArgs &p, hipStream_t s) {
-  const int64_t rows = MODE == GROUP_ROWS ? ceil_div(p.M, p.G) : p.M;
-  const int64_t groups = MODE == GROUP_ROWS ? p.G : 1;
-  if (rows <= 16) {
-    if (groups * ceil_div(p.N, 32) < 256) return launch_stream<MxStream16x16, MODE, KC, IN_MXFP4, OUT>(p, s);
-    return launch_stream<MxStream16, MODE, KC, IN_MXFP4, OUT>(p, s);
-  }
-  if (rows <= 32) return launch_stream<MxStream32, MODE, KC, IN_MXFP4, OUT>(p, s);
-  if (rows >= 192 && workgroups<MODE>(p, 256, 256, 16) >= 256) return launch_tile256<MODE, KC, KC, IN_MXFP4, OUT>(p, s);
-  if (workgroups<MODE>(p, 128, 128) >= 256) return launch_tile<MxTile128, MODE, KC, KC, IN_MXFP4, OUT>(p, s);
-  return launch_tile<MxTile64, MODE, KC, KC, IN_MXFP4, OUT>(p, s);
+  if constexpr (MODE == GROUP_ROWS)
+    return dispatch_mx_groups<OUT>(p, s);
+  else
+    return dispatch_mx_one<OUT>(p, s);
 }
 
 // What both products check; `G`: groups, or 0 for the one product.

@@ -43,27 +43,32 @@ struct TileArgs {
   int c_vec;                                // 16-byte stores to C's rows are aligned
 };
 
-// A workgroup's tile.  Pointers are to the tile's first row and column (of A and
-// B: at k = 0), `rows` and `cols` count from there to the end of the matrix or
-// group, and may be more than the tile's.
+// A workgroup's tile, or its part of one.  Pointers are to the first row and
+// column (of A and B: at k = 0), `rows` and `cols` count from there to the end of
+// the matrix or group, and may be more than the tile's or part's `height` and width.
 struct Where {
   const char *a, *b, *sa, *sb;
   int64_t c;            // element of C
   int rows, cols, K;
-  int skip;             // rows at the tile's start that belong to the group before
+  int skip;             // rows at the start that belong to the group before
+  int height;
 };
 
-// The tile of this workgroup; false if there is none for it.  ALIGN: row tiles
-// of GROUP_ROWS start at multiples of it.
-template <int BM, int BN, int GROUP_M, int MODE, int LA, int LB, int IN, int ALIGN>
+// The tile of this workgroup, or one of up to PARTS parts of it; false if there is
+// none for it.  ALIGN: row tiles of GROUP_ROWS start at multiples of it.
+template <int BM, int BN, int GROUP_M, int MODE, int LA, int LB, int IN, int ALIGN, int PARTS = 1>
 __device__ __forceinline__ bool locate(const TileArgs &p, int lane, Where &w) {
   constexpr int ES2 = IN == IN_MXFP4 ? 1 : 4;          // half bytes of an element
   int tm, tn;
+  Part part;
   if constexpr (MODE == GROUP_ROWS) {
     static_assert(LA == KC, "grouped rows are K-contiguous");
     Group at;
-    if (!find_row_tile<BM, ALIGN>(p.ends, p.G, p.M, p.tiles_n, GROUP_M, (int)blockIdx.x, lane, at, tm, tn)) return false;
-    const int m0 = at.first - early_rows<ALIGN>(at.first) + tm * BM, n0 = tn * BN;
+    if (!find_row_tile<BM, ALIGN, PARTS>(p.ends, p.G, p.M, p.tiles_n, GROUP_M, (int)blockIdx.x, lane, at, part, tm, tn))
+      return false;
+    w.height = BM / part.parts;
+    const int m0 = at.first - early_rows<ALIGN>(at.first) + tm * BM + part.sub * w.height, n0 = tn * BN;
+    if (m0 >= at.last) return false;
     w.a = p.A + m0 * p.lda;
     w.b = p.B + at.g * p.strideb + (LB == KC ? n0 * p.ldb : (int64_t)n0 * ES2 / 2);
     w.c = m0 * p.ldc + n0;
@@ -73,10 +78,15 @@ __device__ __forceinline__ bool locate(const TileArgs &p, int lane, Where &w) {
     return true;
   }
   const int tiles = p.tiles_m * p.tiles_n;
-  int id = xcd_logical_id(blockIdx.x, gridDim.x), g = 0;
-  if constexpr (MODE == GROUP_SUMS) g = id / tiles, id -= g * tiles;
-  tile_coords(id, p.tiles_m, p.tiles_n, GROUP_M, tm, tn);
-  const int m0 = tm * BM, n0 = tn * BN;
+  if (!part_of<PARTS>((int)blockIdx.x, tiles * (MODE == GROUP_SUMS ? p.G : 1), part)) return false;
+  // Group after group, each spread over all the XCDs: with whole groups to an
+  // XCD the one with the most rows keeps the others waiting (16384 rows in eight
+  // uneven groups, 4096 x 4096 fp32: 784 us; so 476, as with even groups).
+  const int g = MODE == GROUP_SUMS ? part.tile / tiles : 0;
+  tile_coords(xcd_logical_id(part.tile - g * tiles, tiles), p.tiles_m, p.tiles_n, GROUP_M, tm, tn);
+  w.height = BM / part.parts;
+  const int m0 = tm * BM + part.sub * w.height, n0 = tn * BN;
+  if (m0 >= p.M) return false;
   w.a = p.A + (LA == KC ? m0 * p.lda : (int64_t)m0 * ES2 / 2);
   w.b = p.B + (LB == KC ? n0 * p.ldb : (int64_t)n0 * ES2 / 2);
   w.c = m0 * p.ldc + n0;

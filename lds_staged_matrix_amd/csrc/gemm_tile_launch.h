@@ -22,22 +22,32 @@ static int64_t workgroups(const TileArgs &p, int bm, int bn, int align = 1) {
   return ceil_div(p.M, bm) * tn * (MODE == GROUP_SUMS ? p.G : 1);
 }
 
+// Tiles that groups of rows have, as far as the host can tell: a group of the mean
+// number of rows ends in half a tile, and one of fewer rows has a tile all the same.
+static int64_t expected_tiles(const TileArgs &p, int bm, int bn) {
+  const int64_t used = p.G < p.M ? p.G : p.M;
+  const int64_t halves = 2 * (int64_t)p.M / bm + used;
+  return (halves > 2 * used ? halves / 2 : used) * ceil_div(p.N, bn);
+}
+
 template <int MODE>
-static hipError_t launch_tiles(const void *kernel, TileArgs p, int bm, int bn, int threads, hipStream_t s, int align = 1) {
+static hipError_t launch_tiles(const void *kernel, TileArgs p, int bm, int bn, int threads, hipStream_t s, int align = 1,
+                               int parts = 1) {
   p.tiles_m = MODE == GROUP_ROWS ? 0 : (int)ceil_div(p.M, bm);
   p.tiles_n = (int)ceil_div(p.N, bn);
   void *params[] = {&p};
-  return hipLaunchKernel(kernel, dim3((unsigned)workgroups<MODE>(p, bm, bn, align)), dim3((unsigned)threads), params, 0, s);
+  const int64_t grid = workgroups_in_parts(workgroups<MODE>(p, bm, bn, align), parts, MODE != GROUP_ROWS);
+  return hipLaunchKernel(kernel, dim3((unsigned)grid), dim3((unsigned)threads), params, 0, s);
 }
 
 template <int MODE, int LA, int LB, int IN, int OUT>
 static hipError_t launch_tile256(const TileArgs &p, hipStream_t s) {
   return launch_tiles<MODE>((const void *)lds_gemm_tile256_kernel<MODE, LA, LB, IN, OUT>, p, 256, 256, 512, s,
-                            tile_align<IN, MODE>());
+                            tile_align<IN, MODE>(), tile256_parts(LA));
 }
 template <class S, int MODE, int LA, int LB, int IN, int OUT>
 static hipError_t launch_tile(const TileArgs &p, hipStream_t s) {
-  return launch_tiles<MODE>((const void *)lds_gemm_tile_kernel<S, MODE, LA, LB, IN, OUT>, p, S::BM, S::BN, S::NT, s);
+  return launch_tiles<MODE>((const void *)lds_gemm_tile_kernel<S, MODE, LA, LB, IN, OUT>, p, S::BM, S::BN, S::NT * S::WK, s);
 }
 template <class S, int MODE, int LB, int IN, int OUT>
 static hipError_t launch_stream(const TileArgs &p, hipStream_t s) {
