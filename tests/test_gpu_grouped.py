@@ -94,9 +94,11 @@ def check_rows(T, groups, N, K, kind, out, layout, how, dist, pad=8, lib=None):
 
 
 HOWS = ["even", "skew", "gaps", "first", "last", "none", "odd"]
-# (T, groups, N, K): a mean of up to 16 and 32 rows, 128 x 128 and 256 x 256 tiles
+# (T, groups, N, K): streams of a mean of up to 16 and 32 rows; few tiles that share K (64 x 64 or 32 x 128, 64 x 128);
+# 128 x 128 alone on a CU, 64 x 128, 128 x 128; 256 x 256 and its parts
 ROWS = [(1, 1, 8, 8), (5, 3, 40, 72), (64, 16, 264, 520), (130, 130, 48, 136), (200, 9, 136, 64), (300, 12, 200, 1032),
-        (700, 5, 400, 328), (1500, 8, 896, 1152), (4096, 4, 4096, 200)]
+        (700, 5, 400, 328), (1500, 8, 896, 1152), (500, 10, 2504, 200), (1000, 20, 2104, 136), (2000, 14, 2104, 136),
+        (2600, 4, 4096, 136), (4096, 4, 4096, 200)]
 
 
 @pytest.mark.parametrize("T,groups,N,K", ROWS)
@@ -122,6 +124,25 @@ def test_rows_odd_columns(N, T):
 
 def test_rows_256_tiles_odd_columns():
     check_rows(5000, 4, 3585, 72, "bf16", "f32", "K", "skew", "int", pad=0)
+
+
+@pytest.mark.parametrize("K", [8, 64, 72, 128, 136, 192, 264, 520])
+@pytest.mark.parametrize("layout", ["K", "MN"])
+def test_rows_256_tiles_by_k(K, layout):
+    """One K tile, two, three and more, cut and whole, in tiles of 256 rows and in parts of 128 and 64."""
+    ends = [256, 256 + 200, 256 + 200 + 128 + 100, 256 + 200 + 228 + 64, 748 + 33, 781 + 700, 1481 + 1]
+    rng = rng_of(K)
+    T, n, N = 1600, len(ends), 2048
+    a, b = integers(rng, (T, K)), integers(rng, (n, N, K))
+    A = padded(a, "bf16")
+    B = padded(b if layout == "K" else np.ascontiguousarray(b.transpose(0, 2, 1)), "bf16")
+    C = torch.full((T, N), -99.0, device="cuda")
+    ok(lsm.gemm_grouped_run(H.handle(), A, B, C, ends_of(ends), n, T, N, K, A.stride(0), B.stride(1), B.stride(0), N,
+                            LAYOUT[layout], lsm.GEMM_BF16_F32, torch.cuda.current_stream()), "gemm_grouped_run")
+    got = R.f64(C)
+    for g, (f, l) in enumerate(G.bounds(ends, T)):
+        assert np.array_equal(got[f:l], a[f:l] @ b[g].T), (g, f, l)
+    assert (got[ends[-1]:] == -99).all()
 
 
 @pytest.mark.parametrize("groups", [63, 64, 65, 200])
@@ -181,7 +202,7 @@ def check_wgrad(T, groups, M, N, kind, out, how, dist, pad=8):
 
 
 WGRAD = [(1, 1, 8, 8), (5, 3, 40, 72), (64, 16, 136, 264), (130, 130, 16, 24), (700, 5, 264, 400), (1500, 8, 1152, 896),
-         (900, 4, 2048, 2056)]
+         (700, 5, 784, 896), (900, 4, 2048, 2056), (2100, 4, 2048, 2056)]
 
 
 @pytest.mark.parametrize("T,groups,M,N", WGRAD)
@@ -263,7 +284,8 @@ def check_mx(T, groups, N, K, out, how, dist, pad=3):
 
 
 MX = [(1, 1, 8, 32), (5, 3, 40, 96), (64, 16, 264, 544), (130, 130, 48, 288), (200, 9, 136, 64), (300, 12, 200, 1056),
-      (700, 5, 400, 320), (1500, 8, 897, 1152), (4100, 4, 4096, 288)]
+      (100, 50, 400, 96), (900, 40, 420, 96), (700, 5, 400, 320), (1500, 8, 897, 1152), (500, 10, 2500, 288),
+      (1000, 20, 2100, 160), (2000, 14, 2100, 288), (4100, 4, 4096, 288)]
 
 
 @pytest.mark.parametrize("T,groups,N,K", MX)

@@ -211,11 +211,12 @@ def check_product(M, N, K, out, dist, pad=3, shift=0):
         R.assert_within(got, ref, bound + R.HALF_STEP[out] * (np.abs(ref) + bound) + R.SMALLEST[out], what)
 
 
-# every kernel: streams of 16 columns and of 32, 17 to 32 rows, 64 x 64, 128 x 128 and 256 x 256 tiles; whole tiles and
-# cut ones, K of one block, of part of a K tile, of many
-PRODUCTS = [(1, 1, 32), (1, 4096, 4096), (3, 37, 64), (16, 130, 544), (7, 9000, 1056), (16, 8200, 2080), (17, 40, 96),
-            (32, 1100, 4128), (33, 64, 288), (100, 65, 32), (64, 64, 256), (250, 300, 1312), (1500, 1152, 896),
-            (2049, 2100, 320), (2048, 2048, 512), (4100, 4097, 288), (4096, 4096, 544)]
+# every kernel: streams of 16, 32 and 64 columns, up to 16 rows and more, tiles that share K (32 x 64, 64 x 64, 64 x 128),
+# 256 x 256 tiles, whole and in parts; whole tiles and cut ones, K of one block, of part of a K tile, of many
+PRODUCTS = [(1, 1, 32), (1, 4096, 4096), (3, 37, 64), (16, 130, 544), (7, 9000, 1056), (16, 8200, 2080), (5, 16400, 96),
+            (17, 40, 96), (32, 1100, 4128), (20, 16400, 96), (33, 64, 288), (100, 65, 32), (64, 64, 256), (250, 300, 1312),
+            (700, 1000, 416), (1500, 1152, 896), (2049, 2100, 320), (2048, 2048, 512), (2048, 2048, 256), (4100, 4097, 288),
+            (4096, 4096, 544)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
