@@ -256,8 +256,8 @@ int gemm_mxfp4_dequantize_run(gemm_handle_t h, const void *Q, const void *S, voi
  *     C[m][n] = round( sum_k qa(m,k) 2^(SA[(k/32)*ldsa + m] - 127)
  *                          * qb(n,k) 2^(SB[(k/32)*ldsb + n] - 127) )
  * Products are exact and summed in fp32 by the matrix cores, with one rounding to
- * C's type: before it an entry is within 2^-22 (K/128 + 8) sum_k |a b| of the
- * formula.  A NaN scale makes its row or column NaN; sums beyond fp32 are
+ * C's type: before it an entry is within 2^-21 (K/128 + 8) sum_k |a b| of the
+ * formula (1e-7 of the result, in the 2-norm, on ordinary data).  A NaN scale makes its row or column NaN; sums beyond fp32 are
  * infinite.
  *   A, SA, B, SB MXFP4 matrices as gemm_mxfp4_quantize_run writes them.  The bytes
  *                between M (N) and the next multiple of 16 in a row of scales
@@ -276,9 +276,9 @@ int gemm_mxfp4_run(gemm_handle_t h, const void *A, const void *B, void *C,
  * ends[g-1] .. ends[g]-1, the first group from row 0.  `ends` are G int32 on the
  * device, read when the work runs; nothing about the groups is known to the host.
  * An end below the ends before it counts as the largest of them, a negative one
- * as 0 and one beyond T as T, so that groups are disjoint and inside the T rows whatever
- * `ends` holds.  Groups may be empty, and rows behind the last group belong to
- * none. */
+ * as 0 and one beyond T as T, so that groups are disjoint and inside the T rows
+ * whatever `ends` holds.  Groups may be empty, and rows behind the last group
+ * belong to none.  G is at most 65536, and `ends` 4-byte aligned. */
 
 /* Enqueue, on `stream`, each group's rows times the group's own matrix:
  *     C[t*ldc + n] = round( sum_k A[t*lda + k] * b(g,k,n) )   for t in group g

@@ -43,18 +43,18 @@ using Stream32MN = StreamShape<32, 128, 2, 2>;
 //    to a CU (1024, 8, 4096, 4096: 74 and 78, alone 84 and 83), and those of up to 96
 //    rows are 64 x 128 (2048, 32, 1152, 896: 20.5 and 20.0, as 128 x 128 23.0 and 22.6).
 template <int LB, int IN, int OUT>
-static hipError_t dispatch_rows(const TileArgs &p, hipStream_t s) {
+static Plan plan_rows(const TileArgs &p) {
   const int64_t mean = ceil_div(p.M, p.G);
-  if (mean <= 16) return launch_stream<std::conditional_t<LB == KC, Stream16, Stream16MN>, GROUP_ROWS, LB, IN, OUT>(p, s);
-  if (mean <= 32) return launch_stream<std::conditional_t<LB == KC, Stream32, Stream32MN>, GROUP_ROWS, LB, IN, OUT>(p, s);
-  if (mean >= 192 && expected_tiles(p, 256, 256) >= 128) return launch_tile256<GROUP_ROWS, KC, LB, IN, OUT>(p, s);
+  if (mean <= 16) return plan_stream<std::conditional_t<LB == KC, Stream16, Stream16MN>, GROUP_ROWS, LB, IN, OUT>();
+  if (mean <= 32) return plan_stream<std::conditional_t<LB == KC, Stream32, Stream32MN>, GROUP_ROWS, LB, IN, OUT>();
+  if (mean >= 192 && expected_tiles(p, 256, 256) >= 128) return plan_tile256<GROUP_ROWS, KC, LB, IN, OUT>();
   if (expected_tiles(p, 64, 128) < 160)
-    return launch_tile<std::conditional_t<LB == KC, SmallSplitK, SmallSplitKMN>, GROUP_ROWS, KC, LB, IN, OUT>(p, s);
+    return plan_tile<std::conditional_t<LB == KC, SmallSplitK, SmallSplitKMN>, GROUP_ROWS, KC, LB, IN, OUT>();
   const int64_t tiles = expected_tiles(p, 128, 128);
-  if (tiles < 192) return launch_tile<Tile64SplitK, GROUP_ROWS, KC, LB, IN, OUT>(p, s);
-  if (tiles <= 264) return launch_tile<Tile128Alone, GROUP_ROWS, KC, LB, IN, OUT>(p, s);
-  if (mean <= 96) return launch_tile<Tile64, GROUP_ROWS, KC, LB, IN, OUT>(p, s);
-  return launch_tile<Tile128, GROUP_ROWS, KC, LB, IN, OUT>(p, s);
+  if (tiles < 192) return plan_tile<Tile64SplitK, GROUP_ROWS, KC, LB, IN, OUT>();
+  if (tiles <= 264) return plan_tile<Tile128Alone, GROUP_ROWS, KC, LB, IN, OUT>();
+  if (mean <= 96) return plan_tile<Tile64, GROUP_ROWS, KC, LB, IN, OUT>();
+  return plan_tile<Tile128, GROUP_ROWS, KC, LB, IN, OUT>();
 }
 
 // The 256 x 256 tile where it fills the CUs and its sums are 512 rows long or more
@@ -67,17 +67,17 @@ using Tile128Sums = TileShape<128, 128, 2, 4, 2>;
 using Tile128SplitK = TileShape<128, 128, 2, 2, 2, 2>;
 
 template <int IN, int OUT>
-static hipError_t dispatch_sums(const TileArgs &p, hipStream_t s) {
+static Plan plan_sums(const TileArgs &p) {
   if (ceil_div(p.K, p.G) >= 512 && workgroups<GROUP_SUMS>(p, 256, 256) >= 256)
-    return launch_tile256<GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
+    return plan_tile256<GROUP_SUMS, MNC, MNC, IN, OUT>();
   const int64_t tiles = workgroups<GROUP_SUMS>(p, 128, 128);
-  if (tiles <= 128) return launch_tile<Tile128SplitK, GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
-  if (tiles <= 256) return launch_tile<Tile128Alone, GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
-  return launch_tile<Tile128Sums, GROUP_SUMS, MNC, MNC, IN, OUT>(p, s);
+  if (tiles <= 128) return plan_tile<Tile128SplitK, GROUP_SUMS, MNC, MNC, IN, OUT>();
+  if (tiles <= 256) return plan_tile<Tile128Alone, GROUP_SUMS, MNC, MNC, IN, OUT>();
+  return plan_tile<Tile128Sums, GROUP_SUMS, MNC, MNC, IN, OUT>();
 }
 
 template <class F>
-static hipError_t with_types(int dtype, F call) {
+static Plan with_types(int dtype, F call) {
   constexpr std::integral_constant<int, IN_BF16> bf16{};
   constexpr std::integral_constant<int, IN_F16> f16{};
   constexpr std::integral_constant<int, OUT_F32> f32{};
@@ -87,14 +87,6 @@ static hipError_t with_types(int dtype, F call) {
     case GEMM_F16_F16: return call(f16, std::integral_constant<int, OUT_F16>{});
     default: return call(f16, f32);
   }
-}
-
-// The smallest tiles, of 16 x 32, must fit a launch of fewer than 2^32 threads of 512 each.
-template <int MODE>
-static bool launch_fits(int64_t M, int64_t N, int64_t G) {
-  const int64_t tm = MODE == GROUP_ROWS ? most_row_tiles(M, G, 16, 1) : ceil_div(M, 128) * G;
-  int64_t n;
-  return !__builtin_mul_overflow(tm, ceil_div(N, MODE == GROUP_ROWS ? 32 : 128), &n) && n < ((int64_t)1 << 23);
 }
 
 }  // namespace lsm
@@ -111,7 +103,7 @@ extern "C" int gemm_grouped_run(gemm_handle_t h, const void *A, const void *B, v
   if (ldc < N || (K > 0 && (lda < K || ldb < (kc ? K : N) || strideb < 0))) return GEMM_ERR_INVALID_ARG;
 
   const bool out_f32 = dtype == GEMM_BF16_F32 || dtype == GEMM_F16_F32;
-  if (G >= kTileMaxDim || T >= kTileMaxDim || N >= kTileMaxDim || K >= kTileMaxDim || ldc >= kTileMaxLd)
+  if (G > kMaxGroups || T >= kTileMaxDim || N >= kTileMaxDim || K >= kTileMaxDim || ldc >= kTileMaxLd)
     return GEMM_ERR_UNSUPPORTED;
   if (((uintptr_t)C & (out_f32 ? 3 : 1)) || ((uintptr_t)ends & 3)) return GEMM_ERR_UNSUPPORTED;
   if (K > 0) {
@@ -119,25 +111,22 @@ extern "C" int gemm_grouped_run(gemm_handle_t h, const void *A, const void *B, v
     if (((uintptr_t)A & 15) || ((uintptr_t)B & 15) || lda % 8 || ldb % 8 || strideb % 8) return GEMM_ERR_UNSUPPORTED;
     if (K % 8 || (!kc && N % 8)) return GEMM_ERR_UNSUPPORTED;
   }
-  if (!launch_fits<GROUP_ROWS>(T, N, G)) return GEMM_ERR_UNSUPPORTED;
   const int64_t c_bytes = footprint_bytes(T, ldc, N, out_f32 ? 4 : 2);
   const int64_t a_bytes = K > 0 ? footprint_bytes(T, lda, K, 2) : 0;
   const int64_t b_bytes = K > 0 ? stacked_bytes(G, 2 * strideb, kc ? footprint_bytes(N, ldb, K, 2) : footprint_bytes(K, ldb, N, 2)) : 0;
   if (c_bytes < 0 || a_bytes < 0 || b_bytes < 0) return GEMM_ERR_UNSUPPORTED;
   if (overlaps_any({C, c_bytes}, {{A, a_bytes}, {B, b_bytes}, {ends, 4 * G}})) return GEMM_ERR_INVALID_ARG;
 
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev != h->device) return GEMM_ERR_DEVICE;
   TileArgs p{};
   p.A = (const char *)A, p.B = (const char *)B, p.C = C, p.ends = ends, p.G = (int)G;
   p.M = (int)T, p.N = (int)N, p.K = (int)K;
   p.lda = 2 * lda, p.ldb = 2 * ldb, p.strideb = 2 * strideb, p.ldc = ldc;
   p.c_vec = (uintptr_t)C % 16 == 0 && ldc * (out_f32 ? 4 : 2) % 16 == 0;
-  const hipError_t e = with_types(dtype, [&](auto in, auto out) {
+  const Plan plan = with_types(dtype, [&](auto in, auto out) {
     constexpr int IN = decltype(in)::value, OUT = decltype(out)::value;
-    return kc ? dispatch_rows<KC, IN, OUT>(p, stream) : dispatch_rows<MNC, IN, OUT>(p, stream);
+    return kc ? plan_rows<KC, IN, OUT>(p) : plan_rows<MNC, IN, OUT>(p);
   });
-  return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+  return run_plan(h, plan, p, stream);
 }
 
 extern "C" int gemm_grouped_wgrad_run(gemm_handle_t h, const void *A, const void *B, void *C, const int32_t *ends,
@@ -151,14 +140,13 @@ extern "C" int gemm_grouped_wgrad_run(gemm_handle_t h, const void *A, const void
 
   const bool out_f32 = dtype == GEMM_BF16_F32 || dtype == GEMM_F16_F32;
   const int64_t size = out_f32 ? 4 : 2;
-  if (G >= kTileMaxDim || T >= kTileMaxDim || M >= kTileMaxDim || N >= kTileMaxDim || ldc >= kTileMaxLd)
+  if (G > kMaxGroups || T >= kTileMaxDim || M >= kTileMaxDim || N >= kTileMaxDim || ldc >= kTileMaxLd)
     return GEMM_ERR_UNSUPPORTED;
   if (((uintptr_t)C & (uintptr_t)(size - 1)) || ((uintptr_t)ends & 3)) return GEMM_ERR_UNSUPPORTED;
   if (T > 0) {
     if (2 * lda >= kTileMaxPitch || 2 * ldb >= kTileMaxPitch) return GEMM_ERR_UNSUPPORTED;
     if (((uintptr_t)A & 15) || ((uintptr_t)B & 15) || lda % 8 || ldb % 8 || M % 8 || N % 8) return GEMM_ERR_UNSUPPORTED;
   }
-  if (!launch_fits<GROUP_SUMS>(M, N, G)) return GEMM_ERR_UNSUPPORTED;
   const int64_t one = footprint_bytes(M, ldc, N, size);
   if (one < 0) return GEMM_ERR_UNSUPPORTED;
   // the groups' results are disjoint
@@ -169,15 +157,13 @@ extern "C" int gemm_grouped_wgrad_run(gemm_handle_t h, const void *A, const void
   if (c_bytes < 0 || a_bytes < 0 || b_bytes < 0) return GEMM_ERR_UNSUPPORTED;
   if (overlaps_any({C, c_bytes}, {{A, a_bytes}, {B, b_bytes}, {ends, 4 * G}})) return GEMM_ERR_INVALID_ARG;
 
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev != h->device) return GEMM_ERR_DEVICE;
   TileArgs p{};
   p.A = (const char *)A, p.B = (const char *)B, p.C = C, p.ends = ends, p.G = (int)G;
   p.M = (int)M, p.N = (int)N, p.K = (int)T;
   p.lda = 2 * lda, p.ldb = 2 * ldb, p.ldc = ldc, p.stridec = G > 1 ? stridec : 0;
   p.c_vec = (uintptr_t)C % 16 == 0 && ldc * size % 16 == 0 && p.stridec * size % 16 == 0;
-  const hipError_t e = with_types(dtype, [&](auto in, auto out) {
-    return dispatch_sums<decltype(in)::value, decltype(out)::value>(p, stream);
+  const Plan plan = with_types(dtype, [&](auto in, auto out) {
+    return plan_sums<decltype(in)::value, decltype(out)::value>(p);
   });
-  return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+  return run_plan(h, plan, p, stream);
 }

@@ -26,10 +26,10 @@ constexpr int mxfp4_out(int dtype) { return dtype == 0 ? OUT_BF16 : dtype == 1 ?
 // row (column) l & 15: one block, with byte OA (OB) of `sa` (`sb`) for its
 // scale.  Each group of lanes l >> 4 holds a block of its own, so that the order
 // of k across the groups only has to be the same for both operands.
-// The instruction's sums keep fp32's bits: over random operands and scales it
-// was off by at most 2^-22 of the sum of sizes, whatever the scales' spread,
-// unlike the fp8 forms (see e4m3_part_as_bf16), because products of one block
-// span eight bits at most.
+// The instruction's sums keep fp32's bits: over 6e7 sums of random and sparse
+// operands, scales that spread over up to 2^60 and running sums from 2^-30 to 2^30
+// times as large it was off by 5.4 * 2^-24 of the sum of sizes at most, unlike
+// the fp8 forms (see e4m3_part_as_bf16): products of one block span eight bits.
 template <int OA, int OB>
 __device__ __forceinline__ v4f32 mfma_mxfp4(v8i16 a, v8i16 b, v4f32 c, int sa, int sb) {
   const auto x = __builtin_bit_cast(u32x4, a), y = __builtin_bit_cast(u32x4, b);

@@ -32,14 +32,14 @@ using MxStream32 = StreamShape<32, 64, 2, 2>;
 // groups, rows, groups, N, K: 64, 16, 4096, 4096: 30.0 in 64 and 32, 37.5 in 16; 240, 8, 4096,
 // 4096: 20.7, as 128 x 128 tiles 24).
 template <int MODE, int OUT>
-static hipError_t dispatch_mx_stream(const TileArgs &p, int64_t rows, int64_t groups, hipStream_t s) {
+static Plan plan_mx_stream(const TileArgs &p, int64_t rows, int64_t groups) {
   const int64_t wide = groups * ceil_div(p.N, 64), half = groups * ceil_div(p.N, 32);
   if (rows > 16)
-    return wide >= 256 ? launch_stream<MxStream32, MODE, KC, IN_MXFP4, OUT>(p, s)
-                       : launch_stream<MxStream32x32, MODE, KC, IN_MXFP4, OUT>(p, s);
-  if (wide >= 256) return launch_stream<MxStream16, MODE, KC, IN_MXFP4, OUT>(p, s);
-  if (half >= 256) return launch_stream<MxStream16x32, MODE, KC, IN_MXFP4, OUT>(p, s);
-  return launch_stream<MxStream16x16, MODE, KC, IN_MXFP4, OUT>(p, s);
+    return wide >= 256 ? plan_stream<MxStream32, MODE, KC, IN_MXFP4, OUT>()
+                       : plan_stream<MxStream32x32, MODE, KC, IN_MXFP4, OUT>();
+  if (wide >= 256) return plan_stream<MxStream16, MODE, KC, IN_MXFP4, OUT>();
+  if (half >= 256) return plan_stream<MxStream16x32, MODE, KC, IN_MXFP4, OUT>();
+  return plan_stream<MxStream16x16, MODE, KC, IN_MXFP4, OUT>();
 }
 
 // One product of more rows: the 256 x 256 tile, whole or in parts, where 128 x 128
@@ -49,38 +49,38 @@ static hipError_t dispatch_mx_stream(const TileArgs &p, int64_t rows, int64_t gr
 // 8192 17.5 in 64 x 64, 22.4 in 64 x 128; 128 x 4096 x 4096 8.4 in 32 x 64, 9.8 in 64 x 64),
 // and up to 64 rows of few columns are streamed (64 x 4096 x 4096 6.7 and 8.3).
 template <int OUT>
-static hipError_t dispatch_mx_one(const TileArgs &p, hipStream_t s) {
+static Plan plan_mx_one(const TileArgs &p) {
   const auto tiles = [&](int bm, int bn) { return ceil_div(p.M, bm) * ceil_div(p.N, bn); };
-  if (p.M <= 32 || (p.M <= 64 && tiles(32, 32) <= 256)) return dispatch_mx_stream<GROUP_NONE, OUT>(p, p.M, 1, s);
-  if (tiles(128, 128) >= 256) return launch_tile256<GROUP_NONE, KC, KC, IN_MXFP4, OUT>(p, s);
-  if (tiles(64, 64) <= 128) return launch_tile<MxTile32SplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>(p, s);
-  if (tiles(64, 64) <= 256) return launch_tile<MxSmallSplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>(p, s);
-  return launch_tile<MxTile64SplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>(p, s);
+  if (p.M <= 32 || (p.M <= 64 && tiles(32, 32) <= 256)) return plan_mx_stream<GROUP_NONE, OUT>(p, p.M, 1);
+  if (tiles(128, 128) >= 256) return plan_tile256<GROUP_NONE, KC, KC, IN_MXFP4, OUT>();
+  if (tiles(64, 64) <= 128) return plan_tile<MxTile32SplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>();
+  if (tiles(64, 64) <= 256) return plan_tile<MxSmallSplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>();
+  return plan_tile<MxTile64SplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>();
 }
 
-// Groups of more rows: as for 16-bit rows (dispatch_rows in gemm_grouped.hip; rows,
+// Groups of more rows: as for 16-bit rows (plan_rows in gemm_grouped.hip; rows,
 // groups, N, K: 2048, 8, 4096, 4096: 38.8 us in 256 x 256, 46 in 128 x 128; 1024, 8, 4096,
 // 4096: 36 and 28; 300, 8, 4096, 4096: 20.0 in 128 x 128 alone, 23.8 in two to a CU; 2048, 32,
 // 1152, 896: 9.9 in 64 x 128, 12.4 in 128 x 128).
 template <int OUT>
-static hipError_t dispatch_mx_groups(const TileArgs &p, hipStream_t s) {
+static Plan plan_mx_groups(const TileArgs &p) {
   const int64_t mean = ceil_div(p.M, p.G);
-  if (mean <= 32) return dispatch_mx_stream<GROUP_ROWS, OUT>(p, mean, p.G < p.M ? p.G : p.M, s);
+  if (mean <= 32) return plan_mx_stream<GROUP_ROWS, OUT>(p, mean, p.G < p.M ? p.G : p.M);
   if (mean >= 192 && expected_tiles(p, 256, 256) >= 128)
-    return launch_tile256<GROUP_ROWS, KC, KC, IN_MXFP4, OUT>(p, s);
-  if (expected_tiles(p, 64, 128) < 160) return launch_tile<MxSmallSplitK, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>(p, s);
+    return plan_tile256<GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
+  if (expected_tiles(p, 64, 128) < 160) return plan_tile<MxSmallSplitK, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
   const int64_t tiles = expected_tiles(p, 128, 128);
-  if (tiles >= 192 && tiles <= 264) return launch_tile<MxTile128Alone, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>(p, s);
-  if (tiles < 192 || mean <= 96) return launch_tile<MxTile64, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>(p, s);
-  return launch_tile<MxTile128, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>(p, s);
+  if (tiles >= 192 && tiles <= 264) return plan_tile<MxTile128Alone, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
+  if (tiles < 192 || mean <= 96) return plan_tile<MxTile64, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
+  return plan_tile<MxTile128, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
 }
 
 template <int MODE, int OUT>
-static hipError_t dispatch_mx(const TileArgs &p, hipStream_t s) {
+static Plan plan_mx(const TileArgs &p) {
   if constexpr (MODE == GROUP_ROWS)
-    return dispatch_mx_groups<OUT>(p, s);
+    return plan_mx_groups<OUT>(p);
   else
-    return dispatch_mx_one<OUT>(p, s);
+    return plan_mx_one<OUT>(p);
 }
 
 // What both products check; `G`: groups, or 0 for the one product.
@@ -92,7 +92,7 @@ static int check_mx(const void *A, const void *B, void *C, const void *SA, const
   if (ldc < N || (K > 0 && (lda < K || ldb < K || ldsa < M || ldsb < N || strideb < 0 || stridesb < 0)))
     return GEMM_ERR_INVALID_ARG;
   const int64_t size = mxfp4_out(dtype) == OUT_F32 ? 4 : 2;
-  if (G >= kTileMaxDim || M >= kTileMaxDim || N >= kTileMaxDim || K >= kTileMaxDim || ldc >= kTileMaxLd)
+  if (G > kMaxGroups || M >= kTileMaxDim || N >= kTileMaxDim || K >= kTileMaxDim || ldc >= kTileMaxLd)
     return GEMM_ERR_UNSUPPORTED;
   if (((uintptr_t)C & (uintptr_t)(size - 1)) || ((uintptr_t)ends & 3)) return GEMM_ERR_UNSUPPORTED;
   if (K > 0) {
@@ -103,11 +103,6 @@ static int check_mx(const void *A, const void *B, void *C, const void *SA, const
         lda % kMxBlock || ldb % kMxBlock || strideb % kMxBlock || ldsa % 16 || ldsb % 16 || stridesb % 16)
       return GEMM_ERR_UNSUPPORTED;
   }
-  // the smallest tiles, 16 x 16, must fit a launch of fewer than 2^32 threads of 512 each
-  int64_t tiles;
-  if (__builtin_mul_overflow(G > 0 ? most_row_tiles(M, G, 16, 1) : ceil_div(M, 16), ceil_div(N, 16), &tiles) ||
-      tiles >= (int64_t)1 << 23)
-    return GEMM_ERR_UNSUPPORTED;
   const int64_t blocks = K / kMxBlock;
   const int64_t c_bytes = footprint_bytes(M, ldc, N, size);
   const int64_t a_bytes = K > 0 ? footprint_bytes(M, lda / 2, K / 2, 1) : 0;
@@ -127,10 +122,8 @@ static int check_mx(const void *A, const void *B, void *C, const void *SA, const
 
 template <int MODE>
 static int run_mx(gemm_handle_t h, const TileArgs &p, int dtype, hipStream_t stream) {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev != h->device) return GEMM_ERR_DEVICE;
-  const hipError_t e = with_out(mxfp4_out(dtype), [&](auto out) { return dispatch_mx<MODE, decltype(out)::value>(p, stream); });
-  return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+  const Plan plan = with_out(mxfp4_out(dtype), [&](auto out) { return plan_mx<MODE, decltype(out)::value>(p); });
+  return run_plan(h, plan, p, stream);
 }
 
 }  // namespace lsm

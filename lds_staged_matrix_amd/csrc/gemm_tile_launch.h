@@ -30,38 +30,59 @@ static int64_t expected_tiles(const TileArgs &p, int bm, int bn) {
   return (halves > 2 * used ? halves / 2 : used) * ceil_div(p.N, bn);
 }
 
-template <int MODE>
-static hipError_t launch_tiles(const void *kernel, TileArgs p, int bm, int bn, int threads, hipStream_t s, int align = 1,
-                               int parts = 1) {
-  p.tiles_m = MODE == GROUP_ROWS ? 0 : (int)ceil_div(p.M, bm);
-  p.tiles_n = (int)ceil_div(p.N, bn);
-  void *params[] = {&p};
-  const int64_t grid = workgroups_in_parts(workgroups<MODE>(p, bm, bn, align), parts, MODE != GROUP_ROWS);
-  return hipLaunchKernel(kernel, dim3((unsigned)grid), dim3((unsigned)threads), params, 0, s);
-}
+// The launch that a product takes.
+struct Plan {
+  const void *kernel;
+  int mode, bm, bn, threads, align, parts;
+};
 
 template <int MODE, int LA, int LB, int IN, int OUT>
-static hipError_t launch_tile256(const TileArgs &p, hipStream_t s) {
-  return launch_tiles<MODE>((const void *)lds_gemm_tile256_kernel<MODE, LA, LB, IN, OUT>, p, 256, 256, 512, s,
-                            tile_align<IN, MODE>(), tile256_parts(LA));
+static Plan plan_tile256() {
+  return {(const void *)lds_gemm_tile256_kernel<MODE, LA, LB, IN, OUT>, MODE, 256, 256, 512, tile_align<IN, MODE>(),
+          tile256_parts(LA)};
 }
 template <class S, int MODE, int LA, int LB, int IN, int OUT>
-static hipError_t launch_tile(const TileArgs &p, hipStream_t s) {
-  return launch_tiles<MODE>((const void *)lds_gemm_tile_kernel<S, MODE, LA, LB, IN, OUT>, p, S::BM, S::BN, S::NT * S::WK, s);
+static Plan plan_tile() {
+  return {(const void *)lds_gemm_tile_kernel<S, MODE, LA, LB, IN, OUT>, MODE, S::BM, S::BN, S::NT * S::WK, 1, 1};
 }
 template <class S, int MODE, int LB, int IN, int OUT>
-static hipError_t launch_stream(const TileArgs &p, hipStream_t s) {
-  return launch_tiles<MODE>((const void *)lds_gemm_stream_kernel<S, MODE, LB, IN, OUT>, p, S::BM, S::BN, 64 * S::WAVES, s);
+static Plan plan_stream() {
+  return {(const void *)lds_gemm_stream_kernel<S, MODE, LB, IN, OUT>, MODE, S::BM, S::BN, 64 * S::WAVES, 1, 1};
 }
 
-// call(OUT) with the output type of an enum gemm_mxfp4_dtype as a constant.
+static int64_t plan_workgroups(const Plan &l, const TileArgs &p) {
+  const int64_t n = l.mode == GROUP_ROWS   ? workgroups<GROUP_ROWS>(p, l.bm, l.bn, l.align)
+                    : l.mode == GROUP_SUMS ? workgroups<GROUP_SUMS>(p, l.bm, l.bn)
+                                           : workgroups<GROUP_NONE>(p, l.bm, l.bn);
+  return workgroups_in_parts(n, l.parts, l.mode != GROUP_ROWS);
+}
+// A launch holds fewer than 2^32 threads.
+static bool plan_fits(const Plan &l, const TileArgs &p) { return plan_workgroups(l, p) < ((int64_t)1 << 32) / l.threads; }
+
+// Enqueue the plan on the handle's device; a gemm_status.
+static int run_plan(gemm_handle_t h, const Plan &l, TileArgs p, hipStream_t stream) {
+  if (!plan_fits(l, p)) return GEMM_ERR_UNSUPPORTED;
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess || dev != h->device) return GEMM_ERR_DEVICE;
+  p.tiles_m = l.mode == GROUP_ROWS ? 0 : (int)ceil_div(p.M, l.bm);
+  p.tiles_n = (int)ceil_div(p.N, l.bn);
+  void *params[] = {&p};
+  return hipLaunchKernel(l.kernel, dim3((unsigned)plan_workgroups(l, p)), dim3((unsigned)l.threads), params, 0, stream) ==
+                 hipSuccess
+             ? GEMM_OK
+             : GEMM_ERR_LAUNCH;
+}
+
+// call(OUT) with the output type as a constant.
 template <class F>
-static hipError_t with_out(int out, F call) {
+static Plan with_out(int out, F call) {
   if (out == OUT_BF16) return call(std::integral_constant<int, OUT_BF16>{});
   if (out == OUT_F16) return call(std::integral_constant<int, OUT_F16>{});
   return call(std::integral_constant<int, OUT_F32>{});
 }
 
+// Groups: a workgroup reads all their ends.
+constexpr int64_t kMaxGroups = (int64_t)1 << 16;
 constexpr int64_t kTileMaxDim = (int64_t)1 << 30, kTileMaxLd = (int64_t)1 << 40;
 // Bytes of an operand's leading dimension: 256 rows of it stay within 2^30.
 constexpr int64_t kTileMaxPitch = (int64_t)1 << 22;

@@ -58,8 +58,9 @@ PRODUCT_CASES = [
     (dict(lda=1 << 23), UNSUPPORTED), (dict(BIG, lda=(1 << 23) - 32), VALID), (dict(ldb=1 << 23), UNSUPPORTED),
     (dict(ldsa=1 << 27), UNSUPPORTED), (dict(BIG, ldsa=(1 << 27) - 16), VALID), (dict(ldc=1 << 40), UNSUPPORTED),
     (dict(M=1 << 30, ldsa=1 << 30), UNSUPPORTED),
-    (dict(BIG, M=1 << 17, N=1 << 14, ldc=1 << 14, ldsa=1 << 17, ldsb=1 << 14), UNSUPPORTED),     # 2^32 threads
-    (dict(BIG, M=1 << 16, N=1 << 14, ldc=1 << 14, ldsa=1 << 17, ldsb=1 << 14), VALID),
+    # 2^32 threads, 512 to a tile of 256 x 256
+    (dict(BIG, M=1 << 26, N=1 << 13, ldc=1 << 13, ldsa=1 << 26, ldsb=1 << 13), UNSUPPORTED),
+    (dict(BIG, M=(1 << 26) - 256, N=1 << 13, ldc=1 << 13, ldsa=1 << 26, ldsb=1 << 13), VALID),
     (dict(C=addr(0) + 636), INVALID), (dict(C=addr(0) + 640), VALID), (dict(C=addr(1) + 1276), INVALID),
     (dict(C=addr(3) + 60), INVALID),                              # 32 + 20 scales, up to a multiple of 16: 64
     (dict(C=addr(3) + 64), VALID), (dict(C=addr(4) + 92), INVALID), (dict(C=addr(4) + 96), VALID),
@@ -82,8 +83,9 @@ ROWS_CASES = [
     (dict(ends=addr(3) + 2), UNSUPPORTED), (dict(lda=1 << 21), UNSUPPORTED), (dict(lda=(1 << 21) - 8, A=1 << 40), VALID),
     (dict(ldb=1 << 21), UNSUPPORTED), (dict(strideb=1 << 40), UNSUPPORTED), (dict(ldc=1 << 40), UNSUPPORTED),
     (dict(T=1 << 30), UNSUPPORTED), (dict(G=1 << 30), UNSUPPORTED), (dict(K=1 << 30, lda=1 << 31, ldb=1 << 31), UNSUPPORTED),
-    (dict(BIG_ROWS := dict(A=1 << 44, B=1 << 47, C=1 << 50, ends=1 << 52), T=1 << 24, N=512, ldc=512, strideb=0), UNSUPPORTED),
-    (dict(BIG_ROWS, T=1 << 23, N=256, ldc=256, strideb=0), VALID),
+    (dict(BIG_ROWS := dict(A=1 << 44, B=1 << 47, C=1 << 50, ends=1 << 52), T=1 << 28, N=8192, ldc=8192, strideb=0), UNSUPPORTED),
+    (dict(BIG_ROWS, T=1 << 26, N=4096, ldc=4096, strideb=0), VALID),
+    (dict(G=1 << 16, ends=1 << 52, strideb=0), VALID), (dict(G=(1 << 16) + 1, ends=1 << 52, strideb=0), UNSUPPORTED),
     (dict(C=addr(0) + 2556), INVALID), (dict(C=addr(0) + 2560), VALID), (dict(C=addr(1) + 15356), INVALID),
     (dict(C=addr(1) + 15360), VALID), (dict(C=addr(3) + 8), INVALID), (dict(C=addr(3) + 12), VALID),
     (dict(C=addr(0), K=0, A=0, B=0), VALID),
