@@ -21,59 +21,78 @@ using Tile128Alone = TileShape<128, 128, 2, 4, 3>;
 using Tile64 = TileShape<64, 128, 2, 2, 2>;
 using Tile64SplitK = TileShape<64, 128, 2, 2, 3, 2>;
 using SmallSplitK = TileShape<64, 64, 2, 2, 3, 2>;
-using SmallSplitKMN = TileShape<32, 128, 1, 4, 3, 2>;
-using Stream16 = StreamShape<16, 64, 4, 2>;
-using Stream32 = StreamShape<32, 64, 4, 2>;
-using Stream16MN = StreamShape<16, 128, 2, 3>;
-using Stream32MN = StreamShape<32, 128, 2, 2>;
+using Tile32SplitK = TileShape<32, 64, 1, 2, 3, 2>;
 
-// By the mean number of rows a group, and by how many tiles are to be expected
-// against the 256 CUs.  Times of uneven groups in bf16, B K- and MN-contiguous
-// (rows, groups, N, K):
-//  * streams up to 32 rows (64, 16, 4096, 4096: 84 and 94 us; 240, 8, 4096, 4096: 58
-//    and 69, as 128 x 128 tiles 69 and 62);
-//  * the 256 x 256 tile and its halves and quarters from 192 rows on (2048, 8, 4096,
-//    4096: 95 and 88 us, as 128 x 128 tiles 125; 16384, 8, 4096, 4096: 435 and 429, 590;
-//    but 1024, 8, 4096, 4096: 84 and 78, 74 and 78);
-//  * few tiles share K out over two groups of waves: 64 x 128 (1500, 8, 896, 1152: 11.9
-//    and 11.7 us; with one group 14.2), fewer still 64 x 64 or 32 x 128 (700, 8, 1152,
-//    896: 8.7 and 8.8; as 64 x 128 10.3);
-//  * tiles of 128 x 128 that are about as many as the CUs stand alone on one, with
-//    three stages (300, 8, 4096, 4096: 50 and 49 us, as 64 x 128 72); more of them go two
-//    to a CU (1024, 8, 4096, 4096: 74 and 78, alone 84 and 83), and those of up to 96
-//    rows are 64 x 128 (2048, 32, 1152, 896: 20.5 and 20.0, as 128 x 128 23.0 and 22.6).
+// Up to 32 rows a group in the mean: the columns of a stream by how many workgroups
+// there are to be (bf16, B K-contiguous; rows, groups, N, K: 1, 1, 2048, 4096: 7.4 us in
+// 16 columns, 8.8 in 32, 10.1 in 64; 2, 2, 4096, 4096: 15.7, 15.5, 18.4; 64, 16, 4096, 4096: 88
+// in 32, 84 in 64; B MN-contiguous, 1, 1, 352, 2344: 8.3 in 64, 15.3 in 128; 16, 8, 4096, 4096:
+// 51 in 64, 43 in 128).
+template <int BM, int LB, int IN, int OUT>
+static Plan plan_few_rows(const TileArgs &p) {
+  const int64_t used = p.G < p.M ? p.G : p.M;
+  const auto columns = [&](int bn) { return used * ceil_div(p.N, bn); };
+  if constexpr (LB == KC) {
+    if (columns(16) <= 256) return plan_stream<StreamShape<BM, 16, 8, 2>, GROUP_ROWS, KC, IN, OUT>();
+    if (columns(32) <= 512) return plan_stream<StreamShape<BM, 32, 4, 2>, GROUP_ROWS, KC, IN, OUT>();
+    return plan_stream<StreamShape<BM, 64, 4, 2>, GROUP_ROWS, KC, IN, OUT>();
+  } else {
+    if (columns(64) < 256) return plan_stream<StreamShape<BM, 64, 4, 2>, GROUP_ROWS, MNC, IN, OUT>();
+    return plan_stream<StreamShape<BM, 128, 2, BM == 16 ? 3 : 2>, GROUP_ROWS, MNC, IN, OUT>();
+  }
+}
+
+// More rows.  Where B's matrices are read for one row tile or two each, HBM
+// sets the pace and loads in flight count: tiles of 128 x 128 that are about as many
+// as the CUs stand alone on one, with three stages (uneven groups in bf16; rows,
+// groups, N, K: 300, 8, 4096, 4096: 50 us, as 64 x 128 72); otherwise groups of up to 96
+// rows take 64 x 128 (2048, 32, 1152, 896: 20.5, as 128 x 128 23.0) and more 128 x 128
+// (1024, 8, 4096, 4096: 74, as 64 x 128 91, in 256 x 256 84).  In all other cases the shape
+// that takes the least by the measured times of K tiles (2048, 8, 4096, 4096: 95 us in
+// 256 x 256, 125 in 128 x 128; 1500, 8, 896, 1152: 11.9 in 64 x 128 with K shared out,
+// without 14.2; 637, 1, 344, 1680: 9.9 in 32 x 64, 12.7 in 32 x 128).
 template <int LB, int IN, int OUT>
 static Plan plan_rows(const TileArgs &p) {
   const int64_t mean = ceil_div(p.M, p.G);
-  if (mean <= 16) return plan_stream<std::conditional_t<LB == KC, Stream16, Stream16MN>, GROUP_ROWS, LB, IN, OUT>();
-  if (mean <= 32) return plan_stream<std::conditional_t<LB == KC, Stream32, Stream32MN>, GROUP_ROWS, LB, IN, OUT>();
-  if (mean >= 192 && expected_tiles(p, 256, 256) >= 128) return plan_tile256<GROUP_ROWS, KC, LB, IN, OUT>();
-  if (expected_tiles(p, 64, 128) < 160)
-    return plan_tile<std::conditional_t<LB == KC, SmallSplitK, SmallSplitKMN>, GROUP_ROWS, KC, LB, IN, OUT>();
-  const int64_t tiles = expected_tiles(p, 128, 128);
-  if (tiles < 192) return plan_tile<Tile64SplitK, GROUP_ROWS, KC, LB, IN, OUT>();
-  if (tiles <= 264) return plan_tile<Tile128Alone, GROUP_ROWS, KC, LB, IN, OUT>();
-  if (mean <= 96) return plan_tile<Tile64, GROUP_ROWS, KC, LB, IN, OUT>();
-  return plan_tile<Tile128, GROUP_ROWS, KC, LB, IN, OUT>();
+  if (mean <= 16) return plan_few_rows<16, LB, IN, OUT>(p);
+  if (mean <= 32) return plan_few_rows<32, LB, IN, OUT>(p);
+  const auto tiles = [&](int bm, int bn) { return expected_tiles(p, bm, bn); };
+  if (p.G > 1 && mean <= 160 && tiles(64, 128) >= 160) {
+    if (tiles(128, 128) >= 192 && tiles(128, 128) <= 264) return plan_tile<Tile128Alone, GROUP_ROWS, KC, LB, IN, OUT>();
+    return mean <= 96 ? plan_tile<Tile64, GROUP_ROWS, KC, LB, IN, OUT>() : plan_tile<Tile128, GROUP_ROWS, KC, LB, IN, OUT>();
+  }
+  const float k = (float)ceil_div(p.K, kTileK(IN));
+  Cheapest c{plan_tile256<GROUP_ROWS, KC, LB, IN, OUT>(),
+             tile256_time({4.5f, 1.6f, 1.03f, 0.85f}, tiles(256, 256), k, tile256_parts(KC))};
+  c.offer(plan_tile<Tile128, GROUP_ROWS, KC, LB, IN, OUT>(),
+          tiles_time(from_hbm(p, {512, 2.5f, 1.15f, 0.7f}, 1.15f, 1.2f), tiles(128, 128), k));
+  c.offer(plan_tile<Tile128Alone, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({256, 2.f, 0.7f, 0.56f}, tiles(128, 128), k));
+  c.offer(plan_tile<Tile64, GROUP_ROWS, KC, LB, IN, OUT>(),
+          tiles_time(from_hbm(p, {768, 2.f, 1.f, 0.55f}, 1.4f, 2.f), tiles(64, 128), k));
+  c.offer(plan_tile<Tile64SplitK, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({256, 1.7f, 0.38f, 0.33f}, tiles(64, 128), k));
+  c.offer(plan_tile<SmallSplitK, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({256, 1.f, 0.25f, 0.24f}, tiles(64, 64), k));
+  c.offer(plan_tile<Tile32SplitK, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({512, 0.6f, 0.29f, 0.18f}, tiles(32, 64), k));
+  return c.plan;
 }
 
-// The 256 x 256 tile where it fills the CUs and its sums are 512 rows long or more
-// in the mean (bf16 to fp32; rows, groups, M, N: 16384, 8, 4096, 4096: 485 us, as 128 x
-// 128 tiles 597; 4096, 8, 2048, 2048: 54 and 57; but 1000, 8, 4096, 4096: 131 and 112).
-// 128 x 128 tiles of which a CU has one or none have three stages (16384, 4, 1024,
-// 1024: 72 us, with two 102), few of them two groups of waves that share the sum out
-// (8192, 2, 512, 512: 47 us; 54 without).
+// The gradient of the matrices: the shape that takes the least for groups of the
+// mean number of rows, C's bytes included in `fixed` (bf16 to fp32; rows, groups, M, N:
+// 16384, 8, 4096, 4096: 485 us in 256 x 256, 597 in 128 x 128; 1000, 8, 4096, 4096: 131 and
+// 112; 16384, 4, 1024, 1024: 102 in 128 x 128 two to a CU, 72 alone).
 using Tile128Sums = TileShape<128, 128, 2, 4, 2>;
-using Tile128SplitK = TileShape<128, 128, 2, 2, 2, 2>;
 
 template <int IN, int OUT>
 static Plan plan_sums(const TileArgs &p) {
-  if (ceil_div(p.K, p.G) >= 512 && workgroups<GROUP_SUMS>(p, 256, 256) >= 256)
-    return plan_tile256<GROUP_SUMS, MNC, MNC, IN, OUT>();
-  const int64_t tiles = workgroups<GROUP_SUMS>(p, 128, 128);
-  if (tiles <= 128) return plan_tile<Tile128SplitK, GROUP_SUMS, MNC, MNC, IN, OUT>();
-  if (tiles <= 256) return plan_tile<Tile128Alone, GROUP_SUMS, MNC, MNC, IN, OUT>();
-  return plan_tile<Tile128Sums, GROUP_SUMS, MNC, MNC, IN, OUT>();
+  const auto tiles = [&](int bm, int bn) { return workgroups<GROUP_SUMS>(p, bm, bn); };
+  const float k = (float)p.K / (float)p.G / (float)kTileK(IN);
+  constexpr float C = OUT == OUT_F32 ? 1.f : 0.5f;             // C's bytes, in fp32's
+  Cheapest c{plan_tile256<GROUP_SUMS, MNC, MNC, IN, OUT>(),
+             tile256_time({3.f + 9.f * C, 1.62f, 1.04f, 1.04f}, tiles(256, 256), k, tile256_parts(MNC))};
+  c.offer(plan_tile<Tile128Sums, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({512, 2.f + 2.f * C, 1.23f, 0.71f}, tiles(128, 128), k));
+  c.offer(plan_tile<Tile128Alone, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({256, 2.f + C, 0.7f, 0.59f}, tiles(128, 128), k));
+  c.offer(plan_tile<Tile64SplitK, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({256, 1.5f + C, 0.35f, 0.34f}, tiles(64, 128), k));
+  c.offer(plan_tile<SmallSplitK, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({256, 0.7f + 0.5f * C, 0.22f, 0.21f}, tiles(64, 64), k));
+  return c.plan;
 }
 
 template <class F>

@@ -126,8 +126,8 @@ __global__ __launch_bounds__(S::NT * S::WK, 2) void lds_gemm_tile_kernel(const T
   constexpr bool MX = IN == IN_MXFP4;
   constexpr int BM = S::BM, BN = S::BN, NS = S::NS, NT = S::NT, WK = S::WK, EB = MX ? 1 : 2;
   constexpr int TM = BM / S::WM, TN = BN / S::WN, FM = TM / 16, FN = TN / 16, KSTEPS = 2;
-  using OA = OperandTile<BM, kTileBytes / EB, LA, NT, EB, 1>;
-  using OB = OperandTile<BN, kTileBytes / EB, LB, NT, EB, 1>;
+  using OA = TileOf<BM, LA, NT, EB>;
+  using OB = TileOf<BN, LB, NT, EB>;
   using GA = ScaleTile<BM, MODE == GROUP_ROWS>;
   using GB = ScaleTile<BN, false>;
   constexpr int SA_AT = OA::BYTES + OB::BYTES, SB_AT = SA_AT + GA::BYTES;
@@ -202,12 +202,12 @@ __global__ __launch_bounds__(S::NT * S::WK, 2) void lds_gemm_tile_kernel(const T
         int ga[FM], gb[FN];
 #pragma unroll
         for (int q = 0; q < FM; q++) {
-          fa[q] = read_frag16<OA>(sA, lane, wm * TM + 16 * q, kk);
+          fa[q] = read_tile_frag<OA>(sA, lane, wm * TM + 16 * q, kk);
           ga[q] = MX ? sa.read(sA + SA_AT, 4 * kk + (lane >> 4), wm * TM + 16 * q + (lane & 15)) : 0;
         }
 #pragma unroll
         for (int q = 0; q < FN; q++) {
-          fb[q] = read_frag16<OB>(sB, lane, wn * TN + 16 * q, kk);
+          fb[q] = read_tile_frag<OB>(sB, lane, wn * TN + 16 * q, kk);
           gb[q] = MX ? sb.read(sA + SB_AT, 4 * kk + (lane >> 4), wn * TN + 16 * q + (lane & 15)) : 0;
         }
         tile_mfma<IN>(acc, fa, fb, ga, gb);
@@ -222,21 +222,6 @@ __global__ __launch_bounds__(S::NT * S::WK, 2) void lds_gemm_tile_kernel(const T
 
 // ------------------------------------------------------------------ streams
 
-// An operand's slab, loaded by one wave: as OperandTile, whose geometry asks for
-// more threads.  A load covers 8 rows of 128 bytes, or 4 of 256.
-template <int MN, int LAYOUT>
-struct SlabTile {
-  static constexpr bool kcontig = LAYOUT == KC, mf16 = !kcontig;
-  static constexpr int ROWS = kcontig ? MN : 64, ROW_BYTES = kcontig ? kTileBytes : 2 * MN;
-  static constexpr int BYTES = ROWS * ROW_BYTES, LOADS = BYTES / 1024, ROW_STEP = 1024 / ROW_BYTES;
-  static constexpr int PHASE_ROWS = 8, LANE_OFFSETS = 2;
-  static_assert(kcontig || ROW_BYTES == 256, "rows of 128 or 256 bytes");
-  __host__ __device__ static constexpr int round_phase(int d) { return d * ROW_STEP / PHASE_ROWS & 1; }
-  __host__ __device__ static constexpr int swizzle(int row) {
-    return kcontig ? kc_swizzle(row, ROW_BYTES) : mn16_swizzle(row, ROW_BYTES);
-  }
-};
-
 template <int BM_, int BN_, int WAVES_, int NS_>
 struct StreamShape {
   static constexpr int BM = BM_, BN = BN_, WAVES = WAVES_, NS = NS_, GROUP_M = 8;
@@ -246,8 +231,8 @@ template <class S, int MODE, int LB, int IN, int OUT>
 __global__ __launch_bounds__(64 * S::WAVES, 2) void lds_gemm_stream_kernel(const TileArgs p) {
   constexpr bool MX = IN == IN_MXFP4;
   constexpr int BM = S::BM, BN = S::BN, NS = S::NS, WAVES = S::WAVES, FM = BM / 16, FN = BN / 16, KSTEPS = 2;
-  using OA = SlabTile<BM, KC>;
-  using OB = SlabTile<BN, LB>;
+  using OA = SlabTile<BM, KC, 64>;
+  using OB = SlabTile<BN, LB, 64>;
   using GA = ScaleTile<BM, MODE == GROUP_ROWS>;
   using GB = ScaleTile<BN, false>;
   constexpr int SA_AT = OA::BYTES + OB::BYTES, SB_AT = SA_AT + GA::BYTES;
@@ -315,12 +300,12 @@ __global__ __launch_bounds__(64 * S::WAVES, 2) void lds_gemm_stream_kernel(const
       for (int kk = 0; kk < KSTEPS; kk++) {
 #pragma unroll
         for (int q = 0; q < FM; q++) {
-          fa[kk][q] = read_frag16<OA>(sA, lane, 16 * q, kk);
+          fa[kk][q] = read_tile_frag<OA>(sA, lane, 16 * q, kk);
           ga[kk][q] = MX ? sa.read(sA + SA_AT, 4 * kk + (lane >> 4), 16 * q + (lane & 15)) : 0;
         }
 #pragma unroll
         for (int q = 0; q < FN; q++) {
-          fb[kk][q] = read_frag16<OB>(sB, lane, 16 * q, kk);
+          fb[kk][q] = read_tile_frag<OB>(sB, lane, 16 * q, kk);
           gb[kk][q] = MX ? sb.read(sA + SB_AT, 4 * kk + (lane >> 4), 16 * q + (lane & 15)) : 0;
         }
       }

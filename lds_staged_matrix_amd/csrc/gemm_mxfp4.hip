@@ -42,37 +42,51 @@ static Plan plan_mx_stream(const TileArgs &p, int64_t rows, int64_t groups) {
   return plan_stream<MxStream16x16, MODE, KC, IN_MXFP4, OUT>();
 }
 
-// One product of more rows: the 256 x 256 tile, whole or in parts, where 128 x 128
-// would fill the CUs (1024 x 8192 x 8192 41 us, as 128 x 128 tiles 47; 1024 x 4096 x
-// 4096 18.1 and 18.4; 512 x 16384 x 4096 24.1 and 29.0); with fewer tiles two groups of
-// waves share K out (256 x 8192 x 8192 21.0 us in 64 x 128, without 32.8; 64 x 16384 x
-// 8192 17.5 in 64 x 64, 22.4 in 64 x 128; 128 x 4096 x 4096 8.4 in 32 x 64, 9.8 in 64 x 64),
-// and up to 64 rows of few columns are streamed (64 x 4096 x 4096 6.7 and 8.3).
+// More rows: the shape that takes the least by the measured times of K tiles (8192
+// x 8192 x 8192 243 us in 256 x 256; 1024 x 8192 x 8192 41 us, as 128 x 128 tiles 47; 512 x
+// 16384 x 4096 24.1 and 29.0; 256 x 8192 x 8192 21.0 in 64 x 128 with K shared out, 32.8
+// without; 2399 x 832 x 4512 19.1 in 64 x 64, 25.6 in 64 x 128; 128 x 4096 x 4096 8.4 in 32 x
+// 64, 9.8 in 64 x 64).
+template <int MODE, int OUT, class Tiles>
+static Plan plan_mx_tiles(const TileArgs &p, Tiles tiles) {
+  const float k = (float)ceil_div(p.K, kTileK(IN_MXFP4));
+  Cheapest c{plan_tile256<MODE, KC, KC, IN_MXFP4, OUT>(),
+             tile256_time({3.f, 2.f, 1.29f, 1.02f}, tiles(256, 256), k, tile256_parts(KC))};
+  c.offer(plan_tile<MxTile128, MODE, KC, KC, IN_MXFP4, OUT>(),
+          tiles_time(from_hbm(p, {512, 2.5f, 1.4f, 0.88f}, 1.15f, 1.2f), tiles(128, 128), k));
+  c.offer(plan_tile<MxTile128Alone, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({256, 1.5f, 0.9f, 0.73f}, tiles(128, 128), k));
+  c.offer(plan_tile<MxTile64, MODE, KC, KC, IN_MXFP4, OUT>(),
+          tiles_time(from_hbm(p, {768, 1.f, 1.37f, 0.84f}, 1.2f, 1.4f), tiles(64, 128), k));
+  c.offer(plan_tile<MxTile64SplitK, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({256, 1.4f, 0.47f, 0.43f}, tiles(64, 128), k));
+  c.offer(plan_tile<MxSmallSplitK, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({256, 0.7f, 0.34f, 0.32f}, tiles(64, 64), k));
+  c.offer(plan_tile<MxTile32SplitK, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({512, 0.3f, 0.47f, 0.26f}, tiles(32, 64), k));
+  return c.plan;
+}
+
+// One product; up to 64 rows of few columns are streamed (64 x 4096 x 4096 6.7 us, in
+// 32 x 64 tiles 8.3).
 template <int OUT>
 static Plan plan_mx_one(const TileArgs &p) {
   const auto tiles = [&](int bm, int bn) { return ceil_div(p.M, bm) * ceil_div(p.N, bn); };
   if (p.M <= 32 || (p.M <= 64 && tiles(32, 32) <= 256)) return plan_mx_stream<GROUP_NONE, OUT>(p, p.M, 1);
-  if (tiles(128, 128) >= 256) return plan_tile256<GROUP_NONE, KC, KC, IN_MXFP4, OUT>();
-  if (tiles(64, 64) <= 128) return plan_tile<MxTile32SplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>();
-  if (tiles(64, 64) <= 256) return plan_tile<MxSmallSplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>();
-  return plan_tile<MxTile64SplitK, GROUP_NONE, KC, KC, IN_MXFP4, OUT>();
+  return plan_mx_tiles<GROUP_NONE, OUT>(p, tiles);
 }
 
-// Groups of more rows: as for 16-bit rows (plan_rows in gemm_grouped.hip; rows,
-// groups, N, K: 2048, 8, 4096, 4096: 38.8 us in 256 x 256, 46 in 128 x 128; 1024, 8, 4096,
-// 4096: 36 and 28; 300, 8, 4096, 4096: 20.0 in 128 x 128 alone, 23.8 in two to a CU; 2048, 32,
-// 1152, 896: 9.9 in 64 x 128, 12.4 in 128 x 128).
+// Groups: as for 16-bit rows (plan_rows in gemm_grouped.hip; uneven groups; rows,
+// groups, N, K: 300, 8, 4096, 4096: 20.0 us in 128 x 128 alone, 23.8 in 64 x 128; 2048, 32, 1152,
+// 896: 9.9 in 64 x 128, 12.4 in 128 x 128; 1024, 8, 4096, 4096: 28 in 128 x 128, 36 in 256 x 256;
+// 2048, 8, 4096, 4096: 46 and 38.8).
 template <int OUT>
 static Plan plan_mx_groups(const TileArgs &p) {
   const int64_t mean = ceil_div(p.M, p.G);
   if (mean <= 32) return plan_mx_stream<GROUP_ROWS, OUT>(p, mean, p.G < p.M ? p.G : p.M);
-  if (mean >= 192 && expected_tiles(p, 256, 256) >= 128)
-    return plan_tile256<GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
-  if (expected_tiles(p, 64, 128) < 160) return plan_tile<MxSmallSplitK, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
-  const int64_t tiles = expected_tiles(p, 128, 128);
-  if (tiles >= 192 && tiles <= 264) return plan_tile<MxTile128Alone, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
-  if (tiles < 192 || mean <= 96) return plan_tile<MxTile64, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
-  return plan_tile<MxTile128, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
+  const auto tiles = [&](int bm, int bn) { return expected_tiles(p, bm, bn); };
+  if (p.G > 1 && mean <= 160 && tiles(64, 128) >= 160) {
+    if (tiles(128, 128) >= 192 && tiles(128, 128) <= 264) return plan_tile<MxTile128Alone, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
+    return mean <= 96 ? plan_tile<MxTile64, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>()
+                      : plan_tile<MxTile128, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
+  }
+  return plan_mx_tiles<GROUP_ROWS, OUT>(p, tiles);
 }
 
 template <int MODE, int OUT>

@@ -100,6 +100,52 @@ __device__ __forceinline__ bool locate(const TileArgs &p, int lane, Where &w) {
   return true;
 }
 
+// ------------------------------------------------- MN-contiguous rows of 64
+//
+// An MN-contiguous tile 64 elements wide has k-rows of 128 bytes, two to a bank
+// line.  One 32-lane phase of the transposed read takes k-rows k..k+3 and
+// k+8..k+11, 32 bytes each (mn16_swizzle in lds_layout.h); four of the eight lie in
+// either half of the line, rows 2 and 8 apart, and the XOR below puts them into its
+// four 32-byte quarters.
+__host__ __device__ constexpr int narrow_swizzle(int k) { return 2 * (((k >> 1) & 1) | ((k >> 2) & 2)); }
+
+// The LDS tile of MN rows or columns of an operand, loaded by NT threads: as
+// OperandTile, for the geometries that it does not take (one wave's loads, of 8
+// rows of 128 bytes or 4 of 256; k-rows of 128 bytes).
+template <int MN, int LAYOUT, int NT>
+struct SlabTile {
+  static constexpr bool kcontig = LAYOUT == KC, mf16 = !kcontig, narrow = !kcontig && MN == 64;
+  static constexpr int ROWS = kcontig ? MN : 64, ROW_BYTES = kcontig ? kTileBytes : 2 * MN;
+  static constexpr int BYTES = ROWS * ROW_BYTES, LOADS = BYTES / (16 * NT), ROW_STEP = 16 * NT / ROW_BYTES;
+  static constexpr int PHASE_ROWS = 8, LANE_OFFSETS = ROW_STEP % 16 == 0 ? 1 : 2;
+  static_assert(kcontig || ROW_BYTES == 256 || ROW_BYTES == 128, "rows of 128 or 256 bytes");
+  static_assert(LOADS >= 1 && (ROW_STEP % 16 == 0 || PHASE_ROWS % ROW_STEP == 0), "one or two swizzle phases");
+  __host__ __device__ static constexpr int round_phase(int d) {
+    return LANE_OFFSETS == 1 ? 0 : d * ROW_STEP / PHASE_ROWS & 1;
+  }
+  __host__ __device__ static constexpr int swizzle(int row) {
+    return kcontig ? kc_swizzle(row, ROW_BYTES) : narrow ? narrow_swizzle(row) : mn16_swizzle(row, ROW_BYTES);
+  }
+};
+template <int MN, int LAYOUT, int NT, int EB>
+using TileOf = std::conditional_t<LAYOUT == MNC && MN == 64, SlabTile<MN, LAYOUT, NT>,
+                                  OperandTile<MN, kTileBytes / EB, LAYOUT, NT, EB, 1>>;
+
+// A 16 x 16 fragment of either (see read_frag16).
+template <class OT>
+__device__ __forceinline__ v8i16 read_tile_frag(const char *lds, int lane, int base, int kk) {
+  if constexpr (!OT::kcontig && OT::ROW_BYTES == 128) {
+    const int k0 = 8 * (lane >> 4) + ((lane >> 2) & 3);          // the k-row, less 32 * kk + 4 * half
+    const char *a = lds + (k0 + 32 * kk) * 128 + 32 * ((base >> 4) ^ (narrow_swizzle(k0) >> 1)) + 16 * ((lane & 3) >> 1) +
+                    8 * (lane & 1);
+    const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)a);
+    const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(a + 4 * 128));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  } else {
+    return read_frag16<OT>(lds, lane, base, kk);
+  }
+}
+
 // ------------------------------------------------------------------- loads
 
 // Bytes of `inner` bytes a row from the first of `outer` rows to the last.

@@ -26,8 +26,44 @@ static int64_t workgroups(const TileArgs &p, int bm, int bn, int align = 1) {
 // number of rows ends in half a tile, and one of fewer rows has a tile all the same.
 static int64_t expected_tiles(const TileArgs &p, int bm, int bn) {
   const int64_t used = p.G < p.M ? p.G : p.M;
+  if (used == 1) return ceil_div(p.M, bm) * ceil_div(p.N, bn);
   const int64_t halves = 2 * (int64_t)p.M / bm + used;
   return (halves > 2 * used ? halves / 2 : used) * ceil_div(p.N, bn);
+}
+
+// What a shape of tiles takes, in microseconds, where operands come from the
+// caches: `fixed` for a round of `slots` workgroups, and for each K tile `full`
+// where the round fills all slots and `half` where it fills half or fewer.  Measured
+// on MI355X with one group whose tiles fill the slots, and half of them, at 16 and
+// 64 K tiles.
+struct Cost {
+  int slots;
+  float fixed, full, half;
+};
+// The same where the groups are so short (up to 512 rows in the mean) that their
+// matrices come from HBM: with one K tile loaded ahead a K tile takes longer by so
+// much.
+static Cost from_hbm(const TileArgs &p, Cost c, float full, float half) {
+  if (p.G > 1 && ceil_div(p.M, p.G) <= 512) c.full *= full, c.half *= half;
+  return c;
+}
+static float round_time(const Cost &c, float share, float ktiles) {
+  return c.fixed + ktiles * (c.half + (c.full - c.half) * (share > 0.5f ? 2 * share - 1 : 0.f));
+}
+static float tiles_time(const Cost &c, int64_t tiles, float ktiles) {
+  const int64_t whole = tiles / c.slots, rest = tiles % c.slots;
+  return (float)whole * round_time(c, 1.f, ktiles) + (rest ? round_time(c, (float)rest / (float)c.slots, ktiles) : 0.f);
+}
+// The 256 x 256 tile, whose last round is cut into parts: `half` and `quarter` are a
+// K tile of so much of a tile.
+struct Cost256 {
+  float fixed, full, half, quarter;
+};
+static float tile256_time(const Cost256 &c, int64_t tiles, float ktiles, int most) {
+  const int64_t rest = tiles % kCUs;
+  const int parts = rest_parts((int)rest, most);
+  const float last = parts == 4 ? c.quarter : parts == 2 ? c.half : c.full;
+  return (float)(tiles / kCUs) * (c.fixed + ktiles * c.full) + (rest ? c.fixed + ktiles * last : 0.f);
 }
 
 // The launch that a product takes.
@@ -49,6 +85,15 @@ template <class S, int MODE, int LB, int IN, int OUT>
 static Plan plan_stream() {
   return {(const void *)lds_gemm_stream_kernel<S, MODE, LB, IN, OUT>, MODE, S::BM, S::BN, 64 * S::WAVES, 1, 1};
 }
+
+// The cheaper of the plans so far and of a shape's.
+struct Cheapest {
+  Plan plan;
+  float time;
+  void offer(const Plan &l, float t) {
+    if (t < time) plan = l, time = t;
+  }
+};
 
 static int64_t plan_workgroups(const Plan &l, const TileArgs &p) {
   const int64_t n = l.mode == GROUP_ROWS   ? workgroups<GROUP_ROWS>(p, l.bm, l.bn, l.align)

@@ -94,11 +94,12 @@ def check_rows(T, groups, N, K, kind, out, layout, how, dist, pad=8, lib=None):
 
 
 HOWS = ["even", "skew", "gaps", "first", "last", "none", "odd"]
-# (T, groups, N, K): streams of a mean of up to 16 and 32 rows; few tiles that share K (64 x 64 or 32 x 128, 64 x 128);
-# 128 x 128 alone on a CU, 64 x 128, 128 x 128; 256 x 256 and its parts
+# (T, groups, N, K): between them every kernel that the host chooses: streams of a mean of up to 16 and 32 rows in 16 to
+# 128 columns; tiles that share K; 64 x 128, 128 x 128, also alone on a CU; 256 x 256 and its parts
 ROWS = [(1, 1, 8, 8), (5, 3, 40, 72), (64, 16, 264, 520), (130, 130, 48, 136), (200, 9, 136, 64), (300, 12, 200, 1032),
         (700, 5, 400, 328), (1500, 8, 896, 1152), (500, 10, 2504, 200), (1000, 20, 2104, 136), (2000, 14, 2104, 136),
-        (2600, 4, 4096, 136), (4096, 4, 4096, 200)]
+        (2600, 4, 4096, 136), (4096, 4, 4096, 200), (40, 40, 400, 64), (664, 40, 416, 64), (365, 20, 224, 64),
+        (8157, 2, 80, 672), (3, 3, 5456, 64), (203, 12, 1400, 64)]
 
 
 @pytest.mark.parametrize("T,groups,N,K", ROWS)
@@ -202,7 +203,7 @@ def check_wgrad(T, groups, M, N, kind, out, how, dist, pad=8):
 
 
 WGRAD = [(1, 1, 8, 8), (5, 3, 40, 72), (64, 16, 136, 264), (130, 130, 16, 24), (700, 5, 264, 400), (1500, 8, 1152, 896),
-         (700, 5, 784, 896), (900, 4, 2048, 2056), (2100, 4, 2048, 2056)]
+         (700, 5, 784, 896), (900, 4, 2048, 2056), (2100, 4, 2048, 2056), (3004, 40, 16, 416), (3218, 8, 144, 7800)]
 
 
 @pytest.mark.parametrize("T,groups,M,N", WGRAD)
@@ -285,7 +286,7 @@ def check_mx(T, groups, N, K, out, how, dist, pad=3):
 
 MX = [(1, 1, 8, 32), (5, 3, 40, 96), (64, 16, 264, 544), (130, 130, 48, 288), (200, 9, 136, 64), (300, 12, 200, 1056),
       (100, 50, 400, 96), (900, 40, 420, 96), (700, 5, 400, 320), (1500, 8, 897, 1152), (500, 10, 2500, 288),
-      (1000, 20, 2100, 160), (2000, 14, 2100, 288), (4100, 4, 4096, 288)]
+      (1000, 20, 2100, 160), (2000, 14, 2100, 288), (4100, 4, 4096, 288), (8013, 40, 1080, 64), (7581, 20, 80, 896)]
 
 
 @pytest.mark.parametrize("T,groups,N,K", MX)
