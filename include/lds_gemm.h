@@ -3,7 +3,12 @@
  * MI355X (gfx950, CDNA4), and of the operators of a quantised linear layer
  * beside it: the RMS norm that makes a product's A operand (gemm_rmsnorm_run),
  * the E4M3 product with row and column scales (gemm_scaled_run) and the
- * product of a few rows with 4-bit weights (gemm_w4_run).
+ * product of a few rows with 4-bit weights (gemm_w4_run); of the products of
+ * rows that belong to groups, each group with a matrix of its own, and their
+ * gradients (gemm_grouped_run, gemm_grouped_wgrad_run); and of MXFP4, 4-bit
+ * floats with a scale for 32 of them: conversions (gemm_mxfp4_quantize_run,
+ * gemm_mxfp4_dequantize_run) and products (gemm_mxfp4_run,
+ * gemm_grouped_mxfp4_run).
  *
  * Operation (gemm_run; the others say theirs): C <- A * B, with
  *     C[m][n] = sum_{k<K} a(m,k) * b(k,n)
@@ -31,7 +36,7 @@
  * Ownership and asynchrony: the caller owns the operands (device memory of
  * the handle's device) and keeps them alive until the work queued on `stream`
  * has finished.  The library never allocates, frees or retains caller
- * memory and allocates no workspace.  The four *_run functions only enqueue
+ * memory and allocates no workspace.  The *_run functions only enqueue
  * work on `stream` and return without synchronising the host; each launches
  * one kernel and nothing else (no allocation, memset or copy), so a call made
  * while `stream` is being captured into a HIP graph is captured and replays.
@@ -39,7 +44,9 @@
  *
  * Errors: every function returns a gemm_status.  Arguments are validated
  * before anything is launched; on an error nothing is enqueued and the outputs
- * are untouched.  No C++ exception crosses this interface.  Handles are
+ * are untouched.  Sizes (M, N, K, T) are below 2^30, leading dimensions and
+ * strides below 2^40 where no smaller limit is given, and no operand spans 2^63
+ * bytes or more.  No C++ exception crosses this interface.  Handles are
  * immutable after creation, so one handle may be used from several host
  * threads and streams at once.  Two operands overlap when the spans from
  * their first to their last element do.
@@ -257,8 +264,8 @@ int gemm_mxfp4_dequantize_run(gemm_handle_t h, const void *Q, const void *S, voi
  *                          * qb(n,k) 2^(SB[(k/32)*ldsb + n] - 127) )
  * Products are exact and summed in fp32 by the matrix cores, with one rounding to
  * C's type: before it an entry is within 2^-21 (K/128 + 8) sum_k |a b| of the
- * formula (1e-7 of the result, in the 2-norm, on ordinary data).  A NaN scale makes its row or column NaN; sums beyond fp32 are
- * infinite.
+ * formula (1e-7 of the result, in the 2-norm, on ordinary data).  A NaN scale makes
+ * its row or column NaN; sums beyond fp32 are infinite.
  *   A, SA, B, SB MXFP4 matrices as gemm_mxfp4_quantize_run writes them.  The bytes
  *                between M (N) and the next multiple of 16 in a row of scales
  *                belong to the array (its last row too), whatever they hold.
