@@ -139,12 +139,22 @@ __device__ __forceinline__ bool find_row_tile(const int32_t *ends, int G, int T,
   return true;
 }
 
-// Group g's rows.
-__device__ __forceinline__ Group find_group(const int32_t *ends, int G, int T, int g, int lane) {
+// Group `at`, or the group at place `at` of an order in which, among each 64, those
+// with more rows (in 16s) come first.
+template <bool BY_SIZE>
+__device__ __forceinline__ Group find_group(const int32_t *ends, int G, int T, int at, int lane) {
   uint32_t end = 0, count = 0;
-  const int chunk = g / 64;
+  const int chunk = at / 64;
   for (int c = 0; c < chunk; c++) GroupChunk<64, 1>(ends, G, T, c, lane, end, count);
-  return GroupChunk<64, 1>(ends, G, T, chunk, lane, end, count).at(chunk, g & 63);
+  const GroupChunk<64, 1> s(ends, G, T, chunk, lane, end, count);
+  if (!BY_SIZE) return s.at(chunk, at & 63);
+  // rows are fewer than 2^30; the lane makes all keys differ, and lanes without a
+  // group come last
+  const uint32_t key = (uint32_t)(s.last - s.first) >> 4 << 6 | (uint32_t)(63 - lane);
+  const int n = G - 64 * chunk < 64 ? G - 64 * chunk : 64;
+  int place = 0;
+  for (int l = 0; l < n; l++) place += (uint32_t)__builtin_amdgcn_readlane((int)key, l) > key;
+  return s.at(chunk, __builtin_ctzll(__ballot(place == (at & 63))));
 }
 
 // The most row tiles that any ends give: a group of r rows has at most

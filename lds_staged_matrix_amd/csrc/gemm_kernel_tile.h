@@ -119,6 +119,7 @@ template <int BM_, int BN_, int WM_, int WN_, int NS_, int WK_ = 1>
 struct TileShape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, WK = WK_, GROUP_M = 8;
   static constexpr int NT = 64 * WM * WN;                // of one group
+  static constexpr int PER_CU = 160 * 1024 / (NS * WK * (BM + BN) * kTileBytes);     // workgroups, by their LDS
 };
 
 template <class S, int MODE, int LA, int LB, int IN, int OUT>

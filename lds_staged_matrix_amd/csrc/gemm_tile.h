@@ -41,6 +41,7 @@ struct TileArgs {
   int64_t ldsa, ldsb, stridesb;             // bytes
   int tiles_m, tiles_n;                     // of one product or group (GROUP_ROWS: tiles_n alone)
   int c_vec;                                // 16-byte stores to C's rows are aligned
+  int by_size;                              // GROUP_SUMS: groups with more rows first
 };
 
 // A workgroup's tile, or its part of one.  Pointers are to the first row and
@@ -81,7 +82,10 @@ __device__ __forceinline__ bool locate(const TileArgs &p, int lane, Where &w) {
   if (!part_of<PARTS>((int)blockIdx.x, tiles * (MODE == GROUP_SUMS ? p.G : 1), part)) return false;
   // Group after group, each spread over all the XCDs: with whole groups to an
   // XCD the one with the most rows keeps the others waiting (16384 rows in eight
-  // uneven groups, 4096 x 4096 fp32: 784 us; so 476, as with even groups).
+  // uneven groups, 4096 x 4096 fp32: 784 us; so 476, as with even groups).  Where not all
+  // tiles run at once the groups with the most rows come first: a long one that
+  // starts last is waited for (16384 rows in eight groups, 1024 x 4096: 157 us, so 131);
+  // in one round the search only takes time (0.1 us for eight groups).
   const int g = MODE == GROUP_SUMS ? part.tile / tiles : 0;
   tile_coords(xcd_logical_id(part.tile - g * tiles, tiles), p.tiles_m, p.tiles_n, GROUP_M, tm, tn);
   w.height = BM / part.parts;
@@ -93,8 +97,9 @@ __device__ __forceinline__ bool locate(const TileArgs &p, int lane, Where &w) {
   w.rows = p.M - m0, w.cols = p.N - n0, w.K = p.K, w.skip = 0;
   if constexpr (IN == IN_MXFP4) w.sa = p.SA + m0, w.sb = p.SB + n0;
   if constexpr (MODE == GROUP_SUMS) {
-    const Group at = find_group(p.ends, p.G, p.K, g, lane);
-    w.a += at.first * p.lda, w.b += at.first * p.ldb, w.c += g * p.stridec;
+    const Group at = p.by_size ? find_group<true>(p.ends, p.G, p.K, g, lane)
+                               : find_group<false>(p.ends, p.G, p.K, g, lane);
+    w.a += at.first * p.lda, w.b += at.first * p.ldb, w.c += at.g * p.stridec;
     w.K = at.last - at.first;
   }
   return true;

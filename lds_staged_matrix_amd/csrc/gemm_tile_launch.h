@@ -69,21 +69,22 @@ static float tile256_time(const Cost256 &c, int64_t tiles, float ktiles, int mos
 // The launch that a product takes.
 struct Plan {
   const void *kernel;
-  int mode, bm, bn, threads, align, parts;
+  int mode, bm, bn, threads, align, parts, slots;       // `slots`: workgroups at once
 };
 
 template <int MODE, int LA, int LB, int IN, int OUT>
 static Plan plan_tile256() {
   return {(const void *)lds_gemm_tile256_kernel<MODE, LA, LB, IN, OUT>, MODE, 256, 256, 512, tile_align<IN, MODE>(),
-          tile256_parts(LA)};
+          tile256_parts(LA), kCUs};
 }
 template <class S, int MODE, int LA, int LB, int IN, int OUT>
 static Plan plan_tile() {
-  return {(const void *)lds_gemm_tile_kernel<S, MODE, LA, LB, IN, OUT>, MODE, S::BM, S::BN, S::NT * S::WK, 1, 1};
+  return {(const void *)lds_gemm_tile_kernel<S, MODE, LA, LB, IN, OUT>, MODE, S::BM, S::BN, S::NT * S::WK, 1, 1,
+          kCUs * S::PER_CU};
 }
 template <class S, int MODE, int LB, int IN, int OUT>
 static Plan plan_stream() {
-  return {(const void *)lds_gemm_stream_kernel<S, MODE, LB, IN, OUT>, MODE, S::BM, S::BN, 64 * S::WAVES, 1, 1};
+  return {(const void *)lds_gemm_stream_kernel<S, MODE, LB, IN, OUT>, MODE, S::BM, S::BN, 64 * S::WAVES, 1, 1, 0};
 }
 
 // The cheaper of the plans so far and of a shape's.
@@ -111,6 +112,7 @@ static int run_plan(gemm_handle_t h, const Plan &l, TileArgs p, hipStream_t stre
   if (hipGetDevice(&dev) != hipSuccess || dev != h->device) return GEMM_ERR_DEVICE;
   p.tiles_m = l.mode == GROUP_ROWS ? 0 : (int)ceil_div(p.M, l.bm);
   p.tiles_n = (int)ceil_div(p.N, l.bn);
+  p.by_size = l.mode == GROUP_SUMS && p.G > 1 && plan_workgroups(l, p) > l.slots;
   void *params[] = {&p};
   return hipLaunchKernel(l.kernel, dim3((unsigned)plan_workgroups(l, p)), dim3((unsigned)l.threads), params, 0, stream) ==
                  hipSuccess

@@ -203,7 +203,8 @@ def check_wgrad(T, groups, M, N, kind, out, how, dist, pad=8):
 
 
 WGRAD = [(1, 1, 8, 8), (5, 3, 40, 72), (64, 16, 136, 264), (130, 130, 16, 24), (700, 5, 264, 400), (1500, 8, 1152, 896),
-         (700, 5, 784, 896), (900, 4, 2048, 2056), (2100, 4, 2048, 2056), (3004, 40, 16, 416), (3218, 8, 144, 7800)]
+         (700, 5, 784, 896), (900, 4, 2048, 2056), (2100, 4, 2048, 2056), (3004, 40, 16, 416), (3218, 8, 144, 7800),
+         (1400, 70, 264, 520), (300, 130, 264, 264)]
 
 
 @pytest.mark.parametrize("T,groups,M,N", WGRAD)
