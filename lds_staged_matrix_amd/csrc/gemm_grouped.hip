@@ -16,25 +16,26 @@ namespace lsm {
 
 // Tiles: rows x columns, waves, LDS stages, groups of waves that share K.  Streams:
 // rows x columns, waves, stages a wave.
-using Tile128 = TileShape<128, 128, 2, 2, 2>;
+using Tile128 = TileShape<128, 128, 2, 4, 2>;
 using Tile128Alone = TileShape<128, 128, 2, 4, 3>;
 using Tile64 = TileShape<64, 128, 2, 2, 2>;
 using Tile64SplitK = TileShape<64, 128, 2, 2, 3, 2>;
-using SmallSplitK = TileShape<64, 64, 2, 2, 3, 2>;
+using Tile64x64 = TileShape<64, 64, 2, 2, 2>;
+using Tile64x64SplitK = TileShape<64, 64, 2, 2, 3, 2>;
 using Tile32SplitK = TileShape<32, 64, 1, 2, 3, 2>;
 
 // Up to 32 rows a group in the mean: the columns of a stream by how many workgroups
 // there are to be (bf16, B K-contiguous; rows, groups, N, K: 1, 1, 2048, 4096: 7.4 us in
-// 16 columns, 8.8 in 32, 10.1 in 64; 2, 2, 4096, 4096: 15.7, 15.5, 18.4; 64, 16, 4096, 4096: 88
-// in 32, 84 in 64; B MN-contiguous, 1, 1, 352, 2344: 8.3 in 64, 15.3 in 128; 16, 8, 4096, 4096:
-// 51 in 64, 43 in 128).
+// 16 columns, 8.8 in 32, 10.1 in 64; 2, 2, 4096, 4096: 15.7, 15.5, 18.4; 4, 4, 4096, 4096: 21.2,
+// 21.3, 19.9; 64, 16, 4096, 4096: 88 in 32, 84 in 64; B MN-contiguous, 1, 1, 352, 2344: 8.3 in
+// 64, 15.3 in 128; 16, 8, 4096, 4096: 51 in 64, 43 in 128).
 template <int BM, int LB, int IN, int OUT>
 static Plan plan_few_rows(const TileArgs &p) {
   const int64_t used = p.G < p.M ? p.G : p.M;
   const auto columns = [&](int bn) { return used * ceil_div(p.N, bn); };
   if constexpr (LB == KC) {
     if (columns(16) <= 256) return plan_stream<StreamShape<BM, 16, 8, 2>, GROUP_ROWS, KC, IN, OUT>();
-    if (columns(32) <= 512) return plan_stream<StreamShape<BM, 32, 4, 2>, GROUP_ROWS, KC, IN, OUT>();
+    if (columns(32) < 512) return plan_stream<StreamShape<BM, 32, 4, 2>, GROUP_ROWS, KC, IN, OUT>();
     return plan_stream<StreamShape<BM, 64, 4, 2>, GROUP_ROWS, KC, IN, OUT>();
   } else {
     if (columns(64) < 256) return plan_stream<StreamShape<BM, 64, 4, 2>, GROUP_ROWS, MNC, IN, OUT>();
@@ -42,56 +43,49 @@ static Plan plan_few_rows(const TileArgs &p) {
   }
 }
 
-// More rows.  Where B's matrices are read for one row tile or two each, HBM
-// sets the pace and loads in flight count: tiles of 128 x 128 that are about as many
-// as the CUs stand alone on one, with three stages (uneven groups in bf16; rows,
-// groups, N, K: 300, 8, 4096, 4096: 50 us, as 64 x 128 72); otherwise groups of up to 96
-// rows take 64 x 128 (2048, 32, 1152, 896: 20.5, as 128 x 128 23.0) and more 128 x 128
-// (1024, 8, 4096, 4096: 74, as 64 x 128 91, in 256 x 256 84).  In all other cases the shape
-// that takes the least by the measured times of K tiles (2048, 8, 4096, 4096: 95 us in
-// 256 x 256, 125 in 128 x 128; 1500, 8, 896, 1152: 11.9 in 64 x 128 with K shared out,
-// without 14.2; 637, 1, 344, 1680: 9.9 in 32 x 64, 12.7 in 32 x 128).
+// More rows: the shape that takes the least (uneven groups in bf16; rows, groups, N, K:
+// 300, 8, 4096, 4096: 50 us in 128 x 128 alone on a CU, 71 in 64 x 128; 2048, 8, 4096, 4096: 93
+// in 256 x 256, 125 in 128 x 128; 6000, 8, 2000, 256: 18.4 in 128 x 128, 20.6 in 64 x 64; 2048, 32,
+// 1152, 896: 20.2 in 64 x 128, 22.8 in 128 x 128; 1500, 8, 896, 1152: 11.7 in 64 x 128 with K
+// shared out, 14.1 without; 767, 1, 448, 1856: 9.5 in 32 x 64, 11.8 in 64 x 64; 722, 16, 552, 3456:
+// 26 in 64 x 64, 36 in 32 x 64).  128 x 128 takes eight waves: four take 5% longer at 256 k
+// and as long at 4096.
 template <int LB, int IN, int OUT>
 static Plan plan_rows(const TileArgs &p) {
   const int64_t mean = ceil_div(p.M, p.G);
   if (mean <= 16) return plan_few_rows<16, LB, IN, OUT>(p);
   if (mean <= 32) return plan_few_rows<32, LB, IN, OUT>(p);
   const auto tiles = [&](int bm, int bn) { return expected_tiles(p, bm, bn); };
-  if (p.G > 1 && mean <= 160 && tiles(64, 128) >= 160) {
-    if (tiles(128, 128) >= 192 && tiles(128, 128) <= 264) return plan_tile<Tile128Alone, GROUP_ROWS, KC, LB, IN, OUT>();
-    return mean <= 96 ? plan_tile<Tile64, GROUP_ROWS, KC, LB, IN, OUT>() : plan_tile<Tile128, GROUP_ROWS, KC, LB, IN, OUT>();
-  }
-  const float k = (float)ceil_div(p.K, kTileK(IN));
+  const float k = k_tiles(p, IN);
   Cheapest c{plan_tile256<GROUP_ROWS, KC, LB, IN, OUT>(),
-             tile256_time({4.5f, 1.6f, 1.03f, 0.85f}, tiles(256, 256), k, tile256_parts(KC))};
-  c.offer(plan_tile<Tile128, GROUP_ROWS, KC, LB, IN, OUT>(),
-          tiles_time(from_hbm(p, {512, 2.5f, 1.15f, 0.7f}, 1.15f, 1.2f), tiles(128, 128), k));
-  c.offer(plan_tile<Tile128Alone, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({256, 2.f, 0.7f, 0.56f}, tiles(128, 128), k));
-  c.offer(plan_tile<Tile64, GROUP_ROWS, KC, LB, IN, OUT>(),
-          tiles_time(from_hbm(p, {768, 2.f, 1.f, 0.55f}, 1.4f, 2.f), tiles(64, 128), k));
-  c.offer(plan_tile<Tile64SplitK, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({256, 1.7f, 0.38f, 0.33f}, tiles(64, 128), k));
-  c.offer(plan_tile<SmallSplitK, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({256, 1.f, 0.25f, 0.24f}, tiles(64, 64), k));
-  c.offer(plan_tile<Tile32SplitK, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({512, 0.6f, 0.29f, 0.18f}, tiles(32, 64), k));
+             tile256_time({5.4f, 1.35f, 0.79f, 0.57f}, tiles(256, 256), k, tile256_parts(KC))};
+  c.offer(plan_tile<Tile128, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({512, 3.7f, 1.22f, 0.77f}, tiles(128, 128), k));
+  c.offer(plan_tile<Tile128Alone, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({256, 3.5f, 0.58f, 0.49f}, tiles(128, 128), k));
+  c.offer(plan_tile<Tile64, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({768, 2.6f, 1.33f, 0.65f}, tiles(64, 128), k));
+  c.offer(plan_tile<Tile64SplitK, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({256, 2.7f, 0.44f, 0.37f}, tiles(64, 128), k));
+  c.offer(plan_tile<Tile64x64SplitK, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({256, 2.f, 0.25f, 0.22f}, tiles(64, 64), k));
+  c.offer(plan_tile<Tile32SplitK, GROUP_ROWS, KC, LB, IN, OUT>(), tiles_time({512, 2.1f, 0.4f, 0.2f}, tiles(32, 64), k));
   return c.plan;
 }
 
 // The gradient of the matrices: the shape that takes the least for groups of the
 // mean number of rows, C's bytes included in `fixed` (bf16 to fp32; rows, groups, M, N:
-// 16384, 8, 4096, 4096: 485 us in 256 x 256, 597 in 128 x 128; 1000, 8, 4096, 4096: 131 and
-// 112; 16384, 4, 1024, 1024: 102 in 128 x 128 two to a CU, 72 alone).
-using Tile128Sums = TileShape<128, 128, 2, 4, 2>;
-
+// 16384, 8, 4096, 4096: 475 us in 256 x 256, 620 in 128 x 128; 1500, 8, 1152, 896: 12.4 in 128 x
+// 128, 17.6 in 256 x 256; 16384, 4, 1024, 1024: 102 in 128 x 128 two to a CU, 72 alone; 59, 7,
+// 1280, 1016: 12.7 in 64 x 64, 16.4 in 128 x 128; 9826, 1, 512, 512: 36 in 64 x 64 with the rows
+// shared out).
 template <int IN, int OUT>
 static Plan plan_sums(const TileArgs &p) {
-  const auto tiles = [&](int bm, int bn) { return workgroups<GROUP_SUMS>(p, bm, bn); };
+  const auto tiles = [&](int bm, int bn) { return (float)workgroups<GROUP_SUMS>(p, bm, bn); };
   const float k = (float)p.K / (float)p.G / (float)kTileK(IN);
   constexpr float C = OUT == OUT_F32 ? 1.f : 0.5f;             // C's bytes, in fp32's
   Cheapest c{plan_tile256<GROUP_SUMS, MNC, MNC, IN, OUT>(),
-             tile256_time({3.f + 9.f * C, 1.62f, 1.04f, 1.04f}, tiles(256, 256), k, tile256_parts(MNC))};
-  c.offer(plan_tile<Tile128Sums, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({512, 2.f + 2.f * C, 1.23f, 0.71f}, tiles(128, 128), k));
-  c.offer(plan_tile<Tile128Alone, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({256, 2.f + C, 0.7f, 0.59f}, tiles(128, 128), k));
-  c.offer(plan_tile<Tile64SplitK, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({256, 1.5f + C, 0.35f, 0.34f}, tiles(64, 128), k));
-  c.offer(plan_tile<SmallSplitK, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({256, 0.7f + 0.5f * C, 0.22f, 0.21f}, tiles(64, 64), k));
+             tile256_time({6.7f + 3.2f * C, 1.7f, 0.86f, 0.86f}, tiles(256, 256), k, tile256_parts(MNC))};
+  c.offer(plan_tile<Tile128, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({512, 2.9f + 1.9f * C, 1.09f, 0.65f}, tiles(128, 128), k));
+  c.offer(plan_tile<Tile128Alone, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({256, 3.7f + 0.4f * C, 0.6f, 0.57f}, tiles(128, 128), k));
+  c.offer(plan_tile<Tile64SplitK, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({256, 2.8f + C, 0.4f, 0.32f}, tiles(64, 128), k));
+  c.offer(plan_tile<Tile64x64, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({1280, 2.5f + 0.8f * C, 1.27f, 0.59f}, tiles(64, 64), k));
+  c.offer(plan_tile<Tile64x64SplitK, GROUP_SUMS, MNC, MNC, IN, OUT>(), tiles_time({256, 2.6f + 1.3f * C, 0.22f, 0.21f}, tiles(64, 64), k));
   return c.plan;
 }
 

@@ -15,11 +15,12 @@
 namespace lsm {
 
 // Shapes as in gemm_grouped.hip.
-using MxTile128 = TileShape<128, 128, 2, 2, 2>;
+using MxTile128 = TileShape<128, 128, 2, 4, 2>;
 using MxTile128Alone = TileShape<128, 128, 2, 4, 3>;
 using MxTile64 = TileShape<64, 128, 2, 2, 2>;
 using MxTile64SplitK = TileShape<64, 128, 2, 2, 3, 2>;
-using MxSmallSplitK = TileShape<64, 64, 2, 2, 3, 2>;
+using MxTile64x64 = TileShape<64, 64, 2, 2, 2>;
+using MxTile64x64SplitK = TileShape<64, 64, 2, 2, 3, 2>;
 using MxTile32SplitK = TileShape<32, 64, 1, 2, 3, 2>;
 using MxStream16x16 = StreamShape<16, 16, 4, 2>;
 using MxStream16x32 = StreamShape<16, 32, 4, 2>;
@@ -42,24 +43,25 @@ static Plan plan_mx_stream(const TileArgs &p, int64_t rows, int64_t groups) {
   return plan_stream<MxStream16x16, MODE, KC, IN_MXFP4, OUT>();
 }
 
-// More rows: the shape that takes the least by the measured times of K tiles (8192
-// x 8192 x 8192 243 us in 256 x 256; 1024 x 8192 x 8192 41 us, as 128 x 128 tiles 47; 512 x
-// 16384 x 4096 24.1 and 29.0; 256 x 8192 x 8192 21.0 in 64 x 128 with K shared out, 32.8
-// without; 2399 x 832 x 4512 19.1 in 64 x 64, 25.6 in 64 x 128; 128 x 4096 x 4096 8.4 in 32 x
-// 64, 9.8 in 64 x 64).
+// More rows: the shape that takes the least (8192 x 8192 x 8192 235 us in 256 x 256; 1024 x
+// 8192 x 8192 41 us, as 128 x 128 tiles 47; 2048 x 2048 x 16384 57 in 128 x 128 alone on a CU, 64 in
+// 128 x 128 two to a CU; 256 x 8192 x 8192 21.0 in 64 x 128 with K shared out, 32.8 without; 2399
+// x 832 x 4512 19.1 in 64 x 64 with K shared out, 25.6 in 64 x 128; 128 x 4096 x 4096 8.4 in 32 x
+// 64, 9.8 in 64 x 64; uneven groups, rows, groups, N, K: 2048, 32, 1152, 896: 9.9 in 64 x 128, 12.2
+// in 128 x 128; 2048, 8, 4096, 4096: 38 in 256 x 256, 46 in 128 x 128; 1225, 4, 733, 352: 6.2 in 64 x
+// 64, 6.8 with K shared out).
 template <int MODE, int OUT, class Tiles>
 static Plan plan_mx_tiles(const TileArgs &p, Tiles tiles) {
-  const float k = (float)ceil_div(p.K, kTileK(IN_MXFP4));
+  const float k = k_tiles(p, IN_MXFP4);
   Cheapest c{plan_tile256<MODE, KC, KC, IN_MXFP4, OUT>(),
-             tile256_time({3.f, 2.f, 1.29f, 1.02f}, tiles(256, 256), k, tile256_parts(KC))};
-  c.offer(plan_tile<MxTile128, MODE, KC, KC, IN_MXFP4, OUT>(),
-          tiles_time(from_hbm(p, {512, 2.5f, 1.4f, 0.88f}, 1.15f, 1.2f), tiles(128, 128), k));
-  c.offer(plan_tile<MxTile128Alone, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({256, 1.5f, 0.9f, 0.73f}, tiles(128, 128), k));
-  c.offer(plan_tile<MxTile64, MODE, KC, KC, IN_MXFP4, OUT>(),
-          tiles_time(from_hbm(p, {768, 1.f, 1.37f, 0.84f}, 1.2f, 1.4f), tiles(64, 128), k));
-  c.offer(plan_tile<MxTile64SplitK, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({256, 1.4f, 0.47f, 0.43f}, tiles(64, 128), k));
-  c.offer(plan_tile<MxSmallSplitK, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({256, 0.7f, 0.34f, 0.32f}, tiles(64, 64), k));
-  c.offer(plan_tile<MxTile32SplitK, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({512, 0.3f, 0.47f, 0.26f}, tiles(32, 64), k));
+             tile256_time({3.6f, 2.f, 1.26f, 0.82f}, tiles(256, 256), k, tile256_parts(KC))};
+  c.offer(plan_tile<MxTile128, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({512, 3.2f, 1.65f, 0.88f}, tiles(128, 128), k));
+  c.offer(plan_tile<MxTile128Alone, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({256, 3.3f, 0.79f, 0.76f}, tiles(128, 128), k));
+  c.offer(plan_tile<MxTile64, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({768, 2.f, 1.5f, 0.76f}, tiles(64, 128), k));
+  c.offer(plan_tile<MxTile64SplitK, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({256, 3.1f, 0.53f, 0.47f}, tiles(64, 128), k));
+  c.offer(plan_tile<MxTile64x64, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({1280, 1.7f, 1.83f, 0.64f}, tiles(64, 64), k));
+  c.offer(plan_tile<MxTile64x64SplitK, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({256, 2.7f, 0.32f, 0.26f}, tiles(64, 64), k));
+  c.offer(plan_tile<MxTile32SplitK, MODE, KC, KC, IN_MXFP4, OUT>(), tiles_time({512, 2.4f, 0.5f, 0.27f}, tiles(32, 64), k));
   return c.plan;
 }
 
@@ -67,26 +69,17 @@ static Plan plan_mx_tiles(const TileArgs &p, Tiles tiles) {
 // 32 x 64 tiles 8.3).
 template <int OUT>
 static Plan plan_mx_one(const TileArgs &p) {
-  const auto tiles = [&](int bm, int bn) { return ceil_div(p.M, bm) * ceil_div(p.N, bn); };
+  const auto tiles = [&](int bm, int bn) { return (float)(ceil_div(p.M, bm) * ceil_div(p.N, bn)); };
   if (p.M <= 32 || (p.M <= 64 && tiles(32, 32) <= 256)) return plan_mx_stream<GROUP_NONE, OUT>(p, p.M, 1);
   return plan_mx_tiles<GROUP_NONE, OUT>(p, tiles);
 }
 
-// Groups: as for 16-bit rows (plan_rows in gemm_grouped.hip; uneven groups; rows,
-// groups, N, K: 300, 8, 4096, 4096: 20.0 us in 128 x 128 alone, 23.8 in 64 x 128; 2048, 32, 1152,
-// 896: 9.9 in 64 x 128, 12.4 in 128 x 128; 1024, 8, 4096, 4096: 28 in 128 x 128, 36 in 256 x 256;
-// 2048, 8, 4096, 4096: 46 and 38.8).
+// Groups, by their mean number of rows.
 template <int OUT>
 static Plan plan_mx_groups(const TileArgs &p) {
   const int64_t mean = ceil_div(p.M, p.G);
   if (mean <= 32) return plan_mx_stream<GROUP_ROWS, OUT>(p, mean, p.G < p.M ? p.G : p.M);
-  const auto tiles = [&](int bm, int bn) { return expected_tiles(p, bm, bn); };
-  if (p.G > 1 && mean <= 160 && tiles(64, 128) >= 160) {
-    if (tiles(128, 128) >= 192 && tiles(128, 128) <= 264) return plan_tile<MxTile128Alone, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
-    return mean <= 96 ? plan_tile<MxTile64, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>()
-                      : plan_tile<MxTile128, GROUP_ROWS, KC, KC, IN_MXFP4, OUT>();
-  }
-  return plan_mx_tiles<GROUP_ROWS, OUT>(p, tiles);
+  return plan_mx_tiles<GROUP_ROWS, OUT>(p, [&](int bm, int bn) { return expected_tiles(p, bm, bn); });
 }
 
 template <int MODE, int OUT>

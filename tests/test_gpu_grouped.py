@@ -99,7 +99,8 @@ HOWS = ["even", "skew", "gaps", "first", "last", "none", "odd"]
 ROWS = [(1, 1, 8, 8), (5, 3, 40, 72), (64, 16, 264, 520), (130, 130, 48, 136), (200, 9, 136, 64), (300, 12, 200, 1032),
         (700, 5, 400, 328), (1500, 8, 896, 1152), (500, 10, 2504, 200), (1000, 20, 2104, 136), (2000, 14, 2104, 136),
         (2600, 4, 4096, 136), (4096, 4, 4096, 200), (40, 40, 400, 64), (664, 40, 416, 64), (365, 20, 224, 64),
-        (8157, 2, 80, 672), (3, 3, 5456, 64), (203, 12, 1400, 64)]
+        (8157, 2, 80, 672), (3, 3, 5456, 64), (203, 12, 1400, 64), (36, 1, 24, 64), (7672, 40, 136, 352),
+        (7903, 12, 136, 352), (1842, 20, 2512, 64), (4430, 40, 1032, 64)]
 
 
 @pytest.mark.parametrize("T,groups,N,K", ROWS)
@@ -204,7 +205,7 @@ def check_wgrad(T, groups, M, N, kind, out, how, dist, pad=8):
 
 WGRAD = [(1, 1, 8, 8), (5, 3, 40, 72), (64, 16, 136, 264), (130, 130, 16, 24), (700, 5, 264, 400), (1500, 8, 1152, 896),
          (700, 5, 784, 896), (900, 4, 2048, 2056), (2100, 4, 2048, 2056), (3004, 40, 16, 416), (3218, 8, 144, 7800),
-         (1400, 70, 264, 520), (300, 130, 264, 264)]
+         (1400, 70, 264, 520), (300, 130, 264, 264), (246, 2, 16, 8496), (262, 2, 80, 16320)]
 
 
 @pytest.mark.parametrize("T,groups,M,N", WGRAD)
@@ -287,7 +288,8 @@ def check_mx(T, groups, N, K, out, how, dist, pad=3):
 
 MX = [(1, 1, 8, 32), (5, 3, 40, 96), (64, 16, 264, 544), (130, 130, 48, 288), (200, 9, 136, 64), (300, 12, 200, 1056),
       (100, 50, 400, 96), (900, 40, 420, 96), (700, 5, 400, 320), (1500, 8, 897, 1152), (500, 10, 2500, 288),
-      (1000, 20, 2100, 160), (2000, 14, 2100, 288), (4100, 4, 4096, 288), (8013, 40, 1080, 64), (7581, 20, 80, 896)]
+      (1000, 20, 2100, 160), (2000, 14, 2100, 288), (4100, 4, 4096, 288), (8013, 40, 1080, 64), (7581, 20, 80, 896),
+      (442, 5, 10776, 64), (37, 1, 24, 8512), (5311, 1, 672, 1696), (7963, 20, 72, 2016)]
 
 
 @pytest.mark.parametrize("T,groups,N,K", MX)
