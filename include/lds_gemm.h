@@ -45,7 +45,7 @@
  * Errors: every function returns a gemm_status.  Arguments are validated
  * before anything is launched; on an error nothing is enqueued and the outputs
  * are untouched.  Sizes (M, N, K, T) are below 2^30, leading dimensions and
- * strides below 2^40 where no smaller limit is given, and no operand spans 2^63
+ * strides below 2^40 where no other limit is given, and no operand spans 2^63
  * bytes or more.  No C++ exception crosses this interface.  Handles are
  * immutable after creation, so one handle may be used from several host
  * threads and streams at once.  Two operands overlap when the spans from
@@ -312,8 +312,8 @@ int gemm_grouped_run(gemm_handle_t h, const void *A, const void *B, void *C,
  * gradient of its C, in the order that gives C the layout wanted.
  *   A, B         bf16 or fp16, 16-byte aligned; lda >= M, ldb >= N, multiples of
  *                8, < 2^21; M and N multiples of 8.
- *   C            aligned to its elements, ldc >= N, stridec >= (M-1)*ldc + N;
- *                overlaps no input.  G == 0, M == 0 or N == 0 is a no-op.
+ *   C            aligned to its elements, ldc >= N, 2^60 > stridec >= (M-1)*ldc + N
+ *                (with one group any); overlaps no input.  G == 0, M == 0 or N == 0 is a no-op.
  *   dtype        as for gemm_grouped_run. */
 int gemm_grouped_wgrad_run(gemm_handle_t h, const void *A, const void *B, void *C,
                            const int32_t *ends, int64_t G, int64_t T, int64_t M, int64_t N,

@@ -28,7 +28,8 @@ using Tile32SplitK = TileShape<32, 64, 1, 2, 3, 2>;
 // there are to be (bf16, B K-contiguous; rows, groups, N, K: 1, 1, 2048, 4096: 7.4 us in
 // 16 columns, 8.8 in 32, 10.1 in 64; 2, 2, 4096, 4096: 15.7, 15.5, 18.4; 4, 4, 4096, 4096: 21.2,
 // 21.3, 19.9; 64, 16, 4096, 4096: 88 in 32, 84 in 64; B MN-contiguous, 1, 1, 352, 2344: 8.3 in
-// 64, 15.3 in 128; 16, 8, 4096, 4096: 51 in 64, 43 in 128).
+// 64, 15.3 in 128; 32, 8, 4096, 4096: 57 in 64, 50 in 128 of four waves, 52 of two with three
+// stages).
 template <int BM, int LB, int IN, int OUT>
 static Plan plan_few_rows(const TileArgs &p) {
   const int64_t used = p.G < p.M ? p.G : p.M;
@@ -39,7 +40,7 @@ static Plan plan_few_rows(const TileArgs &p) {
     return plan_stream<StreamShape<BM, 64, 4, 2>, GROUP_ROWS, KC, IN, OUT>();
   } else {
     if (columns(64) < 256) return plan_stream<StreamShape<BM, 64, 4, 2>, GROUP_ROWS, MNC, IN, OUT>();
-    return plan_stream<StreamShape<BM, 128, 2, BM == 16 ? 3 : 2>, GROUP_ROWS, MNC, IN, OUT>();
+    return plan_stream<StreamShape<BM, 128, BM == 16 ? 4 : 2, 2>, GROUP_ROWS, MNC, IN, OUT>();
   }
 }
 

@@ -25,19 +25,23 @@ using MxTile32SplitK = TileShape<32, 64, 1, 2, 3, 2>;
 using MxStream16x16 = StreamShape<16, 16, 4, 2>;
 using MxStream16x32 = StreamShape<16, 32, 4, 2>;
 using MxStream16 = StreamShape<16, 64, 2, 2>;
+using MxStream16x128 = StreamShape<16, 128, 2, 2>;
 using MxStream32x32 = StreamShape<32, 32, 4, 2>;
 using MxStream32 = StreamShape<32, 64, 2, 2>;
 
 // Streams up to 32 rows, of the widest tiles that give every CU one (1 x 16384 x
 // 8192: 16.1 us in 64 columns, 18.0 in 16; 1 x 4096 x 4096: 5.6 in 16, 6.1 in 32; uneven
-// groups, rows, groups, N, K: 64, 16, 4096, 4096: 30.0 in 64 and 32, 37.5 in 16; 240, 8, 4096,
-// 4096: 20.7, as 128 x 128 tiles 24).
+// groups, rows, groups, N, K: 64, 16, 4096, 4096: 27.1 in 128 columns, 30.5 in 64, 37.5 in 16;
+// 240, 8, 4096, 4096: 20.7, as 128 x 128 tiles 24).  128 columns as long as all run at once,
+// two workgroups to a CU (8, 8, 14336, 4096: 39.7, in 64 columns 34.4).
 template <int MODE, int OUT>
 static Plan plan_mx_stream(const TileArgs &p, int64_t rows, int64_t groups) {
   const int64_t wide = groups * ceil_div(p.N, 64), half = groups * ceil_div(p.N, 32);
   if (rows > 16)
     return wide >= 256 ? plan_stream<MxStream32, MODE, KC, IN_MXFP4, OUT>()
                        : plan_stream<MxStream32x32, MODE, KC, IN_MXFP4, OUT>();
+  const int64_t wider = groups * ceil_div(p.N, 128);
+  if (wider >= 256 && wider <= 512) return plan_stream<MxStream16x128, MODE, KC, IN_MXFP4, OUT>();
   if (wide >= 256) return plan_stream<MxStream16, MODE, KC, IN_MXFP4, OUT>();
   if (half >= 256) return plan_stream<MxStream16x32, MODE, KC, IN_MXFP4, OUT>();
   return plan_stream<MxStream16x16, MODE, KC, IN_MXFP4, OUT>();

@@ -289,7 +289,8 @@ def check_mx(T, groups, N, K, out, how, dist, pad=3):
 MX = [(1, 1, 8, 32), (5, 3, 40, 96), (64, 16, 264, 544), (130, 130, 48, 288), (200, 9, 136, 64), (300, 12, 200, 1056),
       (100, 50, 400, 96), (900, 40, 420, 96), (700, 5, 400, 320), (1500, 8, 897, 1152), (500, 10, 2500, 288),
       (1000, 20, 2100, 160), (2000, 14, 2100, 288), (4100, 4, 4096, 288), (8013, 40, 1080, 64), (7581, 20, 80, 896),
-      (442, 5, 10776, 64), (37, 1, 24, 8512), (5311, 1, 672, 1696), (7963, 20, 72, 2016)]
+      (442, 5, 10776, 64), (37, 1, 24, 8512), (5311, 1, 672, 1696), (7963, 20, 72, 2016),
+      (64, 32, 1032, 288)]
 
 
 @pytest.mark.parametrize("T,groups,N,K", MX)

@@ -217,7 +217,7 @@ PRODUCTS = [(1, 1, 32), (1, 4096, 4096), (3, 37, 64), (16, 130, 544), (7, 9000, 
             (17, 40, 96), (32, 1100, 4128), (20, 16400, 96), (33, 64, 288), (100, 65, 32), (64, 64, 256), (250, 300, 1312),
             (700, 1000, 416), (1500, 1152, 896), (2049, 2100, 320), (2048, 2048, 512), (2048, 2048, 256), (4100, 4097, 288),
             (4096, 4096, 544), (6169, 904, 64), (7670, 72, 864), (355, 5472, 1088), (33, 19152, 2304),
-            (7967, 400, 1664)]
+            (7967, 400, 1664), (3, 32800, 288)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
