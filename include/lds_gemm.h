@@ -263,9 +263,12 @@ int gemm_mxfp4_dequantize_run(gemm_handle_t h, const void *Q, const void *S, voi
  *     C[m][n] = round( sum_k qa(m,k) 2^(SA[(k/32)*ldsa + m] - 127)
  *                          * qb(n,k) 2^(SB[(k/32)*ldsb + n] - 127) )
  * Products are exact and summed in fp32 by the matrix cores, with one rounding to
- * C's type: before it an entry is within 2^-21 (K/128 + 8) sum_k |a b| of the
- * formula (1e-7 of the result, in the 2-norm, on ordinary data).  A NaN scale makes
- * its row or column NaN; sums beyond fp32 are infinite.
+ * C's type: before it an entry is within
+ *     (K/128 + 8) (2^-21 sum_k |a b| + 2^-149)
+ * of the formula (1e-7 of the result, in the 2-norm, on ordinary data), the second
+ * term for products and sums below fp32's normal numbers.  Where sum_k |a b| is
+ * 2^127 or more, sums on the way may overflow: such an entry may be infinite or NaN
+ * whatever the formula gives.  A NaN scale makes its row or column NaN.
  *   A, SA, B, SB MXFP4 matrices as gemm_mxfp4_quantize_run writes them.  The bytes
  *                between M (N) and the next multiple of 16 in a row of scales
  *                belong to the array (its last row too), whatever they hold.
