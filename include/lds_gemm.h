@@ -288,7 +288,9 @@ int gemm_mxfp4_run(gemm_handle_t h, const void *A, const void *B, void *C,
  * An end below the ends before it counts as the largest of them, a negative one
  * as 0 and one beyond T as T, so that groups are disjoint and inside the T rows
  * whatever `ends` holds.  Groups may be empty, and rows behind the last group
- * belong to none.  G is at most 65536, and `ends` 4-byte aligned. */
+ * belong to none.  G is at most 65536, and `ends` 4-byte aligned.  Ends that are
+ * written while the work runs give wrong entries of C (no other memory is read or
+ * written for it, and the work ends). */
 
 /* Enqueue, on `stream`, each group's rows times the group's own matrix:
  *     C[t*ldc + n] = round( sum_k A[t*lda + k] * b(g,k,n) )   for t in group g

@@ -9,6 +9,8 @@
 //
 // Whatever the ends hold, the groups found are disjoint, in order and inside the
 // T rows: an end counts as no less than the ends before it and no more than T.
+// Ends that change while the work runs may leave waves with different tiles, and
+// so with wrong results; each wave still stays inside the T rows and ends.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -129,16 +131,16 @@ __device__ __forceinline__ bool find_row_tile(const int32_t *ends, int G, int T,
   if (!part_of<MOST>(bid, total, part)) return false;
   const int id = xcd_logical_id(part.tile, total), q = id / tiles_n;
   end = count = 0;
-  for (int c = 0;; c++) {
-    if (c > 0 || chunks > 1) s = GroupChunk<BM, ALIGN>(ends, G, T, c, lane, end, count);
+  for (int c = 0; c < chunks; c++) {
+    if (chunks > 1) s = GroupChunk<BM, ALIGN>(ends, G, T, c, lane, end, count);
     const uint64_t past = __ballot(s.through > q);
     if (past) {
       at = s.at(c, __builtin_ctzll(past));
-      break;
+      tile_coords(id - at.before * tiles_n, at.tiles, tiles_n, group_m, tm, tn);
+      return true;
     }
   }
-  tile_coords(id - at.before * tiles_n, at.tiles, tiles_n, group_m, tm, tn);
-  return true;
+  return false;             // the ends have changed since the first pass
 }
 
 // Group `at`, or the group at place `at` of an order in which, among each 64, those
