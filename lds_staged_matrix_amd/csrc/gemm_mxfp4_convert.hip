@@ -111,6 +111,10 @@ __device__ __forceinline__ MxTile mx_tile(const MxArgs &p) {
 template <int T>
 __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const MxArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t scales[kMxBlocks][kMxRows];
+  if constexpr (LSM_LDS_POISON) {   // poison build: all of LDS, before any write
+    lds_poison((char *)scales, sizeof scales, threadIdx.x, 256);
+    __syncthreads();
+  }
   const MxTile t = mx_tile(p);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int k = t.k0 + 8 * lane;
@@ -242,6 +246,10 @@ __device__ __forceinline__ void mx_store8(char *at, uint32_t q, int s) {
 template <int T>
 __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const MxArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t scales[kMxBlocks][kMxRows];
+  if constexpr (LSM_LDS_POISON) {   // poison build: all of LDS, before any write
+    lds_poison((char *)scales, sizeof scales, threadIdx.x, 256);
+    __syncthreads();
+  }
   const MxTile t = mx_tile(p);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int k = t.k0 + 8 * lane;
