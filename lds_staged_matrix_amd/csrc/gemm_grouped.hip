@@ -45,11 +45,11 @@ static Plan plan_few_rows(const TileArgs &p) {
 }
 
 // More rows: the shape that takes the least (uneven groups in bf16; rows, groups, N, K:
-// 300, 8, 4096, 4096: 50 us in 128 x 128 alone on a CU, 71 in 64 x 128; 2048, 8, 4096, 4096: 93
-// in 256 x 256, 125 in 128 x 128; 6000, 8, 2000, 256: 18.4 in 128 x 128, 20.6 in 64 x 64; 2048, 32,
-// 1152, 896: 20.2 in 64 x 128, 22.8 in 128 x 128; 1500, 8, 896, 1152: 11.7 in 64 x 128 with K
-// shared out, 14.1 without; 767, 1, 448, 1856: 9.5 in 32 x 64, 11.8 in 64 x 64; 722, 16, 552, 3456:
-// 26 in 64 x 64, 36 in 32 x 64).  128 x 128 takes eight waves: four take 5% longer at 256 k
+// 300, 8, 4096, 4096: 49 us in 128 x 128 alone on a CU, 67 in 64 x 128; 1500, 4, 4096, 1152: 23
+// in 256 x 256, 28 in 128 x 128; 6000, 16, 1152, 2048: 43 in 128 x 128, 53 in 256 x 256; 2048, 32,
+// 1152, 896: 20.6 in 64 x 128, 24.8 in 128 x 128; 1500, 8, 896, 1152: 12.1 in 64 x 128 with K
+// shared out, 14.2 without; 767, 1, 448, 1856: 9.6 in 32 x 64, 11.9 in 64 x 64; 1500, 8, 512, 2560:
+// 14.8 in 64 x 64, 16.4 in 32 x 64).  128 x 128 takes eight waves: four take 5% longer at 256 k
 // and as long at 4096.
 template <int LB, int IN, int OUT>
 static Plan plan_rows(const TileArgs &p) {
@@ -71,10 +71,10 @@ static Plan plan_rows(const TileArgs &p) {
 
 // The gradient of the matrices: the shape that takes the least for groups of the
 // mean number of rows, C's bytes included in `fixed` (bf16 to fp32; rows, groups, M, N:
-// 16384, 8, 4096, 4096: 475 us in 256 x 256, 620 in 128 x 128; 1500, 8, 1152, 896: 12.4 in 128 x
-// 128, 17.6 in 256 x 256; 16384, 4, 1024, 1024: 102 in 128 x 128 two to a CU, 72 alone; 59, 7,
-// 1280, 1016: 12.7 in 64 x 64, 16.4 in 128 x 128; 9826, 1, 512, 512: 36 in 64 x 64 with the rows
-// shared out).
+// 16384, 8, 4096, 4096: 470-482 us in 256 x 256, 625 in 128 x 128; 1500, 8, 1152, 896: 11.9 in 128 x
+// 128, 19.7 in 256 x 256; 8192, 1, 768, 4096: 81 in 128 x 128 alone on a CU, 107 two to a CU; 59, 7,
+// 1280, 1016: 12.9 in 64 x 64, 16.3 in 128 x 128; with the rows shared out, 9826, 1, 512, 512: 37 in
+// 64 x 64, 55 in 64 x 128; 1500, 1, 1536, 1152: 14.3 in 64 x 128, 17.4 in 64 x 64).
 template <int IN, int OUT>
 static Plan plan_sums(const TileArgs &p) {
   const auto tiles = [&](int bm, int bn) { return (float)workgroups<GROUP_SUMS>(p, bm, bn); };

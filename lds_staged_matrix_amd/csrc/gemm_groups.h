@@ -90,9 +90,11 @@ struct Part {
 
 // The last `rest` tiles that do not fill the 256 CUs once more are cut into up to
 // MOST parts each, as many as still fit one round: a large tile takes long, and a
-// round of few of them as long as a full one (256 x 256 tiles, eight uneven groups of
-// 4096 x 4096: 16384 bf16 rows 445 us, in parts 425; 8192 MXFP4 rows 99 and 89; one MXFP4
-// product of 2048 x 2048 x 8192 49 and 33).
+// round of few of them as long as a full one (256 x 256 tiles: one group of 1500 bf16
+// rows, 4096 x 4096 77 us, in parts 62; four uneven ones, 4096 x 1152 27 and 23; one MXFP4
+// product of 1024 x 8192 x 8192 58 and 45).  With many rounds it hardly shows (16384 bf16
+// rows, eight groups of 4096 x 4096: 442 and 440), and where HBM sets the pace it costs (2048
+// rows, the same matrices: 95 and 100).
 constexpr int kCUs = 256;
 __host__ __device__ constexpr int rest_parts(int rest, int most) {
   return most >= 4 && 4 * rest <= kCUs ? 4 : most >= 2 && 2 * rest <= kCUs ? 2 : 1;

@@ -47,13 +47,14 @@ static Plan plan_mx_stream(const TileArgs &p, int64_t rows, int64_t groups) {
   return plan_stream<MxStream16x16, MODE, KC, IN_MXFP4, OUT>();
 }
 
-// More rows: the shape that takes the least (8192 x 8192 x 8192 235 us in 256 x 256; 1024 x
-// 8192 x 8192 41 us, as 128 x 128 tiles 47; 2048 x 2048 x 16384 57 in 128 x 128 alone on a CU, 64 in
-// 128 x 128 two to a CU; 256 x 8192 x 8192 21.0 in 64 x 128 with K shared out, 32.8 without; 2399
-// x 832 x 4512 19.1 in 64 x 64 with K shared out, 25.6 in 64 x 128; 128 x 4096 x 4096 8.4 in 32 x
-// 64, 9.8 in 64 x 64; uneven groups, rows, groups, N, K: 2048, 32, 1152, 896: 9.9 in 64 x 128, 12.2
-// in 128 x 128; 2048, 8, 4096, 4096: 38 in 256 x 256, 46 in 128 x 128; 1225, 4, 733, 352: 6.2 in 64 x
-// 64, 6.8 with K shared out).
+// More rows: the shape that takes the least (8192 x 8192 x 8192 235-247 us in 256 x 256; 1024 x
+// 8192 x 8192 45 us, as 128 x 128 tiles 51; 2048 x 2048 x 16384 55 in 128 x 128 alone on a CU, 63 in
+// 128 x 128 two to a CU; 256 x 8192 x 8192 20.6 in 64 x 128 with K shared out, 32.4 without; 2399
+// x 832 x 4512 17.3 in 64 x 64, 19.4 in 64 x 128; 1500 x 512 x 8192 14.9 in 64 x 64 with K shared
+// out, 21.3 without; 128 x 4096 x 4096 8.4 in 32 x 64, 9.8 in 64 x 64; uneven groups, rows, groups, N,
+// K: 2048, 32, 1152, 896: 10.0 in 64 x 128, 12.3 in 128 x 128; 6000, 16, 1152, 2560: 21 in 128 x 128,
+// 27 in 256 x 256; 2048, 8, 4096, 4096: 38 in 256 x 256, 47 in 128 x 128; 1225, 4, 733, 352: 6.2 in 64
+// x 64, 6.9 with K shared out).
 template <int MODE, int OUT, class Tiles>
 static Plan plan_mx_tiles(const TileArgs &p, Tiles tiles) {
   const float k = k_tiles(p, IN_MXFP4);

@@ -1,7 +1,8 @@
 """The 256 x 256 kernel of the grouped and of the MXFP4 products (gemm_kernel_tile256.h) in each of its forms: tiles of
 256, 128 and 64 rows, whole, halved and quartered, of one K tile to 18, the last one cut or not; gradients of groups
 without rows and with many, in one round of tiles and in more, the groups in order and by size.  test_kernel_choice.py
-holds that these sizes take this kernel and which forms they reach.  Each case on the library and on the poison
+holds that these sizes take this kernel and which forms they reach (test_gpu_grouped.py's test_rows_256_tiles_by_k is
+served by 64 x 128 and 128 x 128 tiles).  Each case on the library and on the poison
 build, against fp64: bit for bit on integers, and within the bounds of the sums on real values."""
 import pytest
 import torch
