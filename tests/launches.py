@@ -2,8 +2,8 @@
 
 launches(calls): for each call, (entry point's name, arguments behind the handle and before the stream), the kernel's
 name and its grid and block.  A child process makes the calls, on a library whose launches launch_recorder.c
-records.  shape() names the kernels of the grouped and the MXFP4 products shortly, and tiles() tells what the 256 x
-256 kernel computes in a launch."""
+records.  shape() names the kernels of the grouped and the MXFP4 products shortly; tiles_of_rows() and tiles_of_sums() tell
+what the 256 x 256 kernel computes in a launch."""
 import json
 import os
 import re
@@ -14,6 +14,8 @@ import tempfile
 
 import pytest
 
+import lds_staged_matrix_amd as lsm
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 CUS = 256
 
@@ -21,12 +23,15 @@ CUS = 256
 def launches(calls):
     if shutil.which("gcc") is None or shutil.which("c++filt") is None:
         pytest.skip("no gcc or c++filt")
+    if not os.path.exists(lsm.library_path()):
+        from lds_staged_matrix_amd import build
+        build.build()
     with tempfile.TemporaryDirectory() as d:
         recorder = os.path.join(d, "launch_recorder.so")
         subprocess.run(["gcc", "-O1", "-shared", "-fPIC", "-I", "/opt/rocm/include", os.path.join(HERE, "launch_recorder.c"),
                         "-o", recorder], check=True)
         out = subprocess.run([sys.executable, os.path.abspath(__file__), recorder], input=json.dumps(calls), check=True,
-                             capture_output=True, text=True).stdout
+                             capture_output=True, text=True, env=dict(os.environ, PYTHONPATH=os.path.dirname(HERE))).stdout
     made = json.loads(out)
     names = subprocess.run(["c++filt"], input="\n".join(m[0] for m in made), check=True, capture_output=True,
                            text=True).stdout.splitlines()
@@ -110,8 +115,6 @@ def _child(recorder):
     import ctypes
     rec = ctypes.CDLL(recorder, ctypes.RTLD_GLOBAL)
     rec.recorded_kernel.restype = ctypes.c_char_p
-    sys.path.insert(0, os.path.dirname(HERE))
-    import lds_staged_matrix_amd as lsm
     lib = lsm.Library(lsm.library_path())
     device = ctypes.c_int(0)                       # a handle is where its device's number stands
     handle, made = ctypes.cast(ctypes.pointer(device), ctypes.c_void_p), []
